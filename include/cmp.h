@@ -199,7 +199,8 @@ CMP_API int cmp_compressor_noalloc(const cmp_bf16* x, float* kv_state, float* sc
 /* Synchronises stream, then returns and clears the error word the kernels of
  * the current device set: CMP_OK, CMP_ERR_DEVICE_INDEX or CMP_ERR_TIMEOUT
  * (CMP_ERR_CUDA if the synchronisation itself fails). Covers the calls made on
- * `stream` and every cmp_compressor_noalloc call on the current device. */
+ * `stream` and, on the current device, every cmp_compressor_noalloc,
+ * cmp_kv_append and cmp_paged_attention call that has finished. */
 CMP_API int cmp_get_error(void* stream);
 
 /* Bytes of device workspace a call with these shapes uses (the two-phase
@@ -266,6 +267,149 @@ CMP_API int cmp_nsa_compress(const void* input, const void* weight, const int32_
                              int64_t page_block_size, void* output_cache, void* stream,
                              const cmp_nsa_dims* dims);
 
+/* ---- the paged cache: filling it and attending over it -----------------------
+ * cmp_qk_norm_rope, cmp_kv_append and cmp_paged_attention work on 16-bit tensors
+ * (dtype CMP_NSA_FP16 or CMP_NSA_BF16) and on a pair of paged caches, k_cache and
+ * v_cache [block_num, page_size, Hk, D]: the layout of cmp_nsa_compress's paged
+ * input, so the cache that cmp_kv_append fills is one that cmp_nsa_compress
+ * compresses. Position p of sequence b is row p % page_size of block
+ * block_table[b][p / page_size]. Packed tokens: sequence b owns rows
+ * cu_seqlens[b] .. cu_seqlens[b+1]-1 at positions start_pos[b], start_pos[b]+1, ...
+ *
+ * Tensors of tokens (q, k, v) have their last two dimensions dense and any token
+ * stride that is a multiple of 8 elements (parts of one projection's output). All
+ * 16-bit and float32 tensors start on 16-byte boundaries, int32 ones on 4-byte ones.
+ *
+ * cu_seqlens[B] may be below T: tokens behind the last sequence are skipped, their
+ * rows of the caches, out and lse left as they were (batches padded to a captured
+ * size). None of the three uses the library's per-stream workspace or allocates
+ * memory, so they may be captured at any time and run on several streams at once.
+ * What their kernels find wrong (cu_seqlens not rising from 0 or past T, a
+ * negative start_pos, positions past INT32_MAX, a needed table entry outside
+ * [0, block_num) or past table_stride) never faults: the access is skipped and an
+ * error word of the device is set, which cmp_get_error reports (on any stream of
+ * that device) and clears. B == 0 or T == 0 is a successful no-op. */
+
+/* The position rotation of the last `dim` channels of a head (cmp_compressor's
+ * tables, one row per token):
+ *   sin, cos  device [T, dim], float32 (CMP_ROPE_F32) or bf16 (CMP_ROPE_BF16)
+ *   dim       a multiple of 16, at most D; 0: no rotation (sin, cos are not read)
+ *   pairs     CMP_ROPE_INTERLEAVED: channels (2j, 2j+1) of the rotated part;
+ *             CMP_ROPE_HALVES: channels (j, dim/2 + j). The pair (a, b) becomes
+ *             (a cos[j] - b sin[j], b cos[dim/2+j] + a sin[dim/2+j]). */
+enum { CMP_ROPE_INTERLEAVED = 0, CMP_ROPE_HALVES = 1 };
+enum { CMP_ROPE_F32 = 0, CMP_ROPE_BF16 = 1 };
+typedef struct cmp_rope {
+  const void* sin;
+  const void* cos;
+  int32_t dim;
+  int32_t pairs;
+  int32_t dtype;
+} cmp_rope;
+
+typedef struct cmp_qk_dims {
+  int64_t T;                      /* tokens */
+  int64_t Hq, Hk;                 /* query heads 1..1024, key heads 0 (no keys)..1024 */
+  int64_t D;                      /* channels per head, a multiple of 16, at most 256 */
+  int64_t q_stride, k_stride;     /* elements from one token to the next */
+  int64_t q_out_stride, k_out_stride;
+} cmp_qk_dims;
+
+/* Norms of queries and keys for each head with the position rotation in the same
+ * pass: y = x / sqrt(mean(x^2) + eps) * weight over a head's D channels, then the
+ * rotation; fp32 inside, one rounding to dtype.
+ *   q, k            device [T, Hq, D], [T, Hk, D]; k, k_weight, k_out unused if Hk == 0
+ *   q_weight, k_weight  device [D], dtype
+ *   rope            host pointer, NULL: no rotation
+ *   q_out, k_out    device, as q and k; may be q and k themselves (in place, equal
+ *                   strides), must not overlap them otherwise
+ * Returns CMP_OK, CMP_ERR_NULLPTR, CMP_ERR_INVALID, CMP_ERR_UNSUPPORTED (dtype,
+ * rotation kind) or CMP_ERR_CUDA. */
+CMP_API int cmp_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight,
+                             const cmp_rope* rope, float eps, int32_t dtype, void* q_out, void* k_out,
+                             void* stream, const cmp_qk_dims* dims);
+
+typedef struct cmp_kv_dims {
+  int64_t B;                   /* sequences */
+  int64_t T;                   /* tokens: rows of k and v */
+  int64_t Hk;                  /* key heads, 1..256 */
+  int64_t D;                   /* channels per head, a multiple of 16, at most 256 */
+  int64_t k_stride, v_stride;  /* elements from one token to the next */
+  int64_t block_num;           /* blocks of each cache; block_num * page_size <= INT32_MAX */
+  int64_t page_size;           /* rows per block, 1..1024 */
+  int64_t table_stride;        /* columns of block_table */
+} cmp_kv_dims;
+
+/* Stores every token's keys (normed as in cmp_qk_norm_rope if norm_weight is not
+ * NULL, rotated if rope says so) and values (unchanged) at its position of its
+ * sequence's cache rows. No other row changes. Requirement that the library does
+ * not check: two tokens of a call never map to one row (sequences that are
+ * written do not share the blocks they are written to).
+ *   k, v          device [T, Hk, D]
+ *   norm_weight   device [D] or NULL
+ *   block_table   device int32 [B, table_stride]; entries a call does not need are
+ *                 not read
+ *   cu_seqlens    device int32 [B+1];  start_pos  device int32 [B], NULL: all 0
+ *   k_cache, v_cache  device [block_num, page_size, Hk, D], updated in place
+ * Returns as cmp_qk_norm_rope does. */
+CMP_API int cmp_kv_append(const void* k, const void* v, const void* norm_weight, const cmp_rope* rope, float eps,
+                          const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* start_pos,
+                          int32_t dtype, void* k_cache, void* v_cache, void* stream, const cmp_kv_dims* dims);
+
+typedef struct cmp_attn_dims {
+  int64_t B;             /* sequences */
+  int64_t T;             /* tokens: rows of q; T * Hq <= INT32_MAX */
+  int64_t Hq, Hk;        /* query heads 1..1024, key heads 1..256; Hq = G * Hk with G <= 128 */
+  int64_t D;             /* channels per head, a multiple of 16, at most 256 */
+  int64_t q_stride;      /* elements from one token of q to the next */
+  int64_t block_num;     /* blocks of each cache; block_num * page_size <= INT32_MAX */
+  int64_t page_size;     /* rows per block: a multiple of 16, at most 1024 */
+  int64_t table_stride;  /* columns of block_table */
+  int64_t max_len;       /* no sequence of the call has more tokens (0: T) */
+} cmp_attn_dims;
+
+/* Attention of the call's tokens over their sequences' cached keys and values.
+ * Query head h reads key head h / G. The token at position p (start_pos[b] + its
+ * index) sees the first n(p) cache rows of its sequence,
+ *   n(p) = 0 if p + 1 < key_block, else (p + 1 - key_block) / key_stride + 1,
+ * of those the last `window` if window > 0:
+ *   key_block = key_stride = 1: plain causal attention; the cache holds the chunk's
+ *     own keys too (cmp_kv_append comes before);
+ *   key_block = key_stride = ratio: rows that the Compressor made of `ratio` positions;
+ *   key_block = compress_block_size, key_stride = compress_stride: NSA's rows.
+ *   out = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j)
+ * A row that sees no key gets out = 0, lse = -inf. lse joins attentions over
+ * different caches (raw and compressed rows, windows): the weights exp(lse_i - lse)
+ * of their outs. Scores, statistics and sums are fp32; the weights are rounded to
+ * dtype before the product with v, and out once at the end.
+ *   q            device [T, Hq, D];  out  device [T, Hq, D], dense
+ *   k_cache, v_cache  device [block_num, page_size, Hk, D]; rows that no token of
+ *                the call sees may hold anything (NaN too). Inside one call a
+ *                non-finite value may reach rows that do not see its key.
+ *   block_table  device int32 [B, table_stride]; entries of rows that no token sees
+ *                are not used (may be -1). Sequences may share blocks.
+ *   cu_seqlens   device int32 [B+1];  start_pos  device int32 [B], NULL: all 0
+ *   scale        finite, > 0
+ *   window       keys, 0: no window;  key_block, key_stride  1..INT32_MAX
+ *   lse          device float32 [T, Hq] or NULL
+ *   workspace    device, workspace_bytes >= cmp_paged_attention_workspace(dims), 16-byte
+ *                aligned; its contents need no preparation and mean nothing afterwards.
+ *                Calls that may overlap need one each.
+ * A sequence longer than max_len, or whose cu_seqlens or start_pos entries are not
+ * usable, is skipped and reported (its rows are left as they were); a missing
+ * table entry reads as zeros and is reported. Results do not depend on timing
+ * (no floating-point atomics).
+ * Returns CMP_OK, CMP_ERR_NULLPTR, CMP_ERR_INVALID, CMP_ERR_UNSUPPORTED (dtype) or
+ * CMP_ERR_CUDA (launch, or the driver cannot describe the cache as a TMA tensor). */
+CMP_API int cmp_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                                const int32_t* cu_seqlens, const int32_t* start_pos, float scale, int64_t window,
+                                int64_t key_block, int64_t key_stride, int32_t dtype, void* out, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream, const cmp_attn_dims* dims);
+
+/* Bytes of workspace such a call needs on the current device (0: invalid dims).
+ * Depends on D, Hq / Hk and max_len (or T) only. Host only. */
+CMP_API size_t cmp_paged_attention_workspace(const cmp_attn_dims* dims);
+
 /* ---- measurement --------------------------------------------------------
  * Kernels of the library, by id: */
 enum {
@@ -281,7 +425,11 @@ enum {
                                   that each own 16 channels */
   CMP_KERNEL_NSA = 9,          /* NsaCompressWithCache */
   CMP_KERNEL_NSA_SCAN = 10,    /* NsaCompressWithCache, packed layout: each batch's first row */
-  CMP_KERNEL_COUNT = 11
+  CMP_KERNEL_QK_NORM_ROPE = 11,
+  CMP_KERNEL_KV_APPEND = 12,
+  CMP_KERNEL_ATTN_DECODE = 13,  /* paged attention, few rows per key head */
+  CMP_KERNEL_ATTN_COMBINE = 14, /* paged attention: joins rows that were cut between CTAs */
+  CMP_KERNEL_COUNT = 15
 };
 
 /* Name of a kernel id (NULL if out of range). */

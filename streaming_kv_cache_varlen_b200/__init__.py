@@ -22,7 +22,8 @@ CMP_OK = 0
 STATUS = {0: "CMP_OK", 1: "CMP_ERR_NULLPTR", 2: "CMP_ERR_INVALID", 3: "CMP_ERR_UNSUPPORTED",
           4: "CMP_ERR_CUDA", 5: "CMP_ERR_DEVICE_INDEX", 6: "CMP_ERR_TIMEOUT"}
 KERNELS = ("sched", "proj_tcgen05", "proj_mma_sync", "proj_decode", "pool_epilogue",
-           "fused_tcgen05", "finish", "decode_fused", "decode_cp", "nsa_compress", "nsa_scan")
+           "fused_tcgen05", "finish", "decode_fused", "decode_cp", "nsa_compress", "nsa_scan",
+           "qk_norm_rope", "kv_append", "attn_decode", "attn_combine")
 
 
 class CmpError(RuntimeError):
@@ -41,6 +42,26 @@ class cmp_nsa_dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("D", ctypes.c_int64),
                 ("tokens", ctypes.c_int64), ("table_stride", ctypes.c_int64),
                 ("result_len", ctypes.c_int64)]
+
+
+class cmp_rope(ctypes.Structure):
+    _fields_ = [("sin", ctypes.c_void_p), ("cos", ctypes.c_void_p), ("dim", ctypes.c_int32),
+                ("pairs", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class cmp_qk_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("T", "Hq", "Hk", "D", "q_stride", "k_stride", "q_out_stride",
+                                              "k_out_stride")]
+
+
+class cmp_kv_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hk", "D", "k_stride", "v_stride", "block_num", "page_size",
+                                              "table_stride")]
+
+
+class cmp_attn_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("B", "T", "Hq", "Hk", "D", "q_stride", "block_num", "page_size",
+                                              "table_stride", "max_len")]
 
 
 def _load() -> ctypes.CDLL:
@@ -69,6 +90,13 @@ def _load() -> ctypes.CDLL:
         "cmp_debug_unreachable_barrier": (ctypes.c_int, [ctypes.c_int]),
         "cmp_nsa_compress": (ctypes.c_int, [P, P, P, P, P, I32, I32, I64, I64, I64, P, P,
                                             ctypes.POINTER(cmp_nsa_dims)]),
+        "cmp_qk_norm_rope": (ctypes.c_int, [P] * 4 + [ctypes.POINTER(cmp_rope), ctypes.c_float, I32, P, P, P,
+                                                      ctypes.POINTER(cmp_qk_dims)]),
+        "cmp_kv_append": (ctypes.c_int, [P] * 3 + [ctypes.POINTER(cmp_rope), ctypes.c_float, P, P, P, I32, P, P, P,
+                                                   ctypes.POINTER(cmp_kv_dims)]),
+        "cmp_paged_attention": (ctypes.c_int, [P] * 6 + [ctypes.c_float, I64, I64, I64, I32, P, P, P, SZ, P,
+                                                         ctypes.POINTER(cmp_attn_dims)]),
+        "cmp_paged_attention_workspace": (SZ, [ctypes.POINTER(cmp_attn_dims)]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -242,6 +270,246 @@ def nsa_compress(input, weight, slot_mapping, act_seq_len, output_cache, *, comp
     if st != CMP_OK:
         raise CmpError(st, "cmp_nsa_compress")
     return output_cache
+
+
+_ROPE_PAIRS = {"interleaved": 0, "halves": 1}
+_DTYPE = {}  # torch dtype -> CMP_NSA_FP16 / CMP_NSA_BF16, filled on first use
+
+
+def _dtype16(t, name) -> int:
+    import torch
+    if not _DTYPE:
+        _DTYPE.update({torch.float16: 0, torch.bfloat16: 1})
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    if t.dtype not in _DTYPE:
+        raise TypeError(f"{name} must be float16 or bfloat16")
+    return _DTYPE[t.dtype]
+
+
+def _check_tokens(t, name, dtype, shape, device) -> int:
+    """[T, H, D] with the last two dimensions dense; returns the token stride in elements."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or tuple(t.shape[1:]) != tuple(shape[1:]) or (shape[0] is not None and t.shape[0] != shape[0]):
+        raise ValueError(f"{name} must be {['T' if s is None else s for s in shape]}, got {list(t.shape)}")
+    H, D = t.shape[1], t.shape[2]
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"the last two dimensions of {name} must be dense")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    stride = t.stride(0) if t.shape[0] > 1 else H * D
+    if stride < H * D or stride % 8 or t.data_ptr() % 16:
+        raise ValueError(f"{name}: tokens must start on 16-byte boundaries, {H * D} or more elements apart")
+    return stride
+
+
+def _rope(sin, cos, pairs, T, D, device):
+    """cmp_rope of the tables, or None."""
+    import torch
+    if pairs not in _ROPE_PAIRS:
+        raise ValueError(f"rope_pairs must be one of {sorted(_ROPE_PAIRS)}")
+    if sin is None and cos is None:
+        return None
+    if sin is None or cos is None:
+        raise ValueError("sin and cos come together")
+    if sin.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("sin and cos must be float32 or bfloat16")
+    for t, name in ((sin, "sin"), (cos, "cos")):
+        _check(t, name, sin.dtype, 2, device)
+    R = sin.shape[1]
+    if tuple(sin.shape) != (T, R) or sin.shape != cos.shape or R < 16 or R % 16 or R > D:
+        raise ValueError(f"sin and cos must both be [{T}, dim] with dim a multiple of 16, at most {D}")
+    return cmp_rope(_ptr(sin), _ptr(cos), R, _ROPE_PAIRS[pairs], 0 if sin.dtype == torch.float32 else 1)
+
+
+def _handle(stream, dev):
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight=None, *, sin=None, cos=None, rope_pairs: str = "interleaved",
+                 eps: float = 1e-6, q_out=None, k_out=None, stream=None):
+    """Norms of queries and keys for each head with the position rotation in the same
+    pass (see cmp_qk_norm_rope in include/cmp.h); returns ``(q_out, k_out)``.
+
+    q [T, Hq, D], k [T, Hk, D] or None, fp16 / bf16, last two dimensions dense; q_weight,
+    k_weight [D] of the same dtype; sin / cos [T, dim] float32 or bf16 (the last dim
+    channels of a head are rotated; None: no rotation), ``rope_pairs`` "interleaved"
+    (channels 2j, 2j+1) or "halves" (j, dim/2 + j). ``q_out`` / ``k_out`` may be q / k
+    (in place); new dense tensors by default."""
+    import torch
+    dt = _dtype16(q, "q")
+    dev = q.device
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    qs = _check_tokens(q, "q", q.dtype, (T, Hq, D), dev)
+    _check(q_weight, "q_weight", q.dtype, 1, dev)
+    Hk = ks = kos = 0
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3 or k_weight is None:
+            raise ValueError("k must be [T, Hk, D] and comes with k_weight")
+        Hk = k.shape[1]
+        ks = _check_tokens(k, "k", q.dtype, (T, Hk, D), dev)
+        _check(k_weight, "k_weight", q.dtype, 1, dev)
+    if q_weight.shape[0] != D or (k is not None and k_weight.shape[0] != D):
+        raise ValueError(f"the weights must be [{D}]")
+    rope = _rope(sin, cos, rope_pairs, T, D, dev)
+    handle = _handle(stream, dev)
+    if (q_out is None or (k is not None and k_out is None)) and stream is not None:
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, dev)):
+            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if q_out is None else q_out
+            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev) if k is not None and k_out is None else k_out
+    else:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if q_out is None else q_out
+        k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev) if k is not None and k_out is None else k_out
+    qos = _check_tokens(q_out, "q_out", q.dtype, (T, Hq, D), dev)
+    if k is not None:
+        kos = _check_tokens(k_out, "k_out", q.dtype, (T, Hk, D), dev)
+    dims = cmp_qk_dims(T, Hq, Hk, D, qs, ks, qos, kos)
+    with torch.cuda.device(dev):
+        st = lib.cmp_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight) if k is not None else None,
+                                  None if rope is None else ctypes.byref(rope), eps, dt, _ptr(q_out),
+                                  _ptr(k_out) if k is not None else None, handle, ctypes.byref(dims))
+    if st != CMP_OK:
+        raise CmpError(st, "cmp_qk_norm_rope")
+    return q_out, (k_out if k is not None else None)
+
+
+def _check_cache(k_cache, v_cache, dtype, Hk, D, dev):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _check(t, name, dtype, 4, dev)
+    if k_cache.shape != v_cache.shape or tuple(k_cache.shape[2:]) != (Hk, D):
+        raise ValueError(f"k_cache and v_cache must both be [block_num, page_size, {Hk}, {D}]")
+
+
+def _check_sequences(block_table, cu_seqlens, start_pos, dev) -> int:
+    import torch
+    i32 = torch.int32
+    _check(block_table, "block_table", i32, 2, dev)
+    _check(cu_seqlens, "cu_seqlens", i32, 1, dev)
+    B = cu_seqlens.shape[0] - 1
+    if B < 0 or block_table.shape[0] != B:
+        raise ValueError("cu_seqlens must be [B + 1] and block_table [B, table_stride]")
+    if start_pos is not None:
+        _check(start_pos, "start_pos", i32, 1, dev)
+        if start_pos.shape[0] != B:
+            raise ValueError("start_pos must be [B]")
+    return B
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, cu_seqlens, start_pos=None, *, norm_weight=None, sin=None,
+              cos=None, rope_pairs: str = "interleaved", eps: float = 1e-6, stream=None):
+    """Keys (normed if ``norm_weight`` is given, rotated if ``sin`` / ``cos`` are) and values
+    into the paged caches at their sequences' next positions (see cmp_kv_append in
+    include/cmp.h); updates and returns ``(k_cache, v_cache)``.
+
+    k, v [T, Hk, D] fp16 / bf16, last two dimensions dense; caches [block_num, page_size,
+    Hk, D]; block_table int32 [B, pages]; cu_seqlens int32 [B+1]; start_pos int32 [B] or
+    None; norm_weight [D]; sin / cos [T, dim] float32 or bf16, as for ``qk_norm_rope``."""
+    import torch
+    dt = _dtype16(k, "k")
+    dev = k.device
+    if k.dim() != 3:
+        raise ValueError("k must be [T, Hk, D]")
+    T, Hk, D = k.shape
+    ks = _check_tokens(k, "k", k.dtype, (T, Hk, D), dev)
+    vs = _check_tokens(v, "v", k.dtype, (T, Hk, D), dev)
+    _check_cache(k_cache, v_cache, k.dtype, Hk, D, dev)
+    B = _check_sequences(block_table, cu_seqlens, start_pos, dev)
+    if norm_weight is not None:
+        _check(norm_weight, "norm_weight", k.dtype, 1, dev)
+        if norm_weight.shape[0] != D:
+            raise ValueError(f"norm_weight must be [{D}]")
+    rope = _rope(sin, cos, rope_pairs, T, D, dev)
+    dims = cmp_kv_dims(B, T, Hk, D, ks, vs, k_cache.shape[0], k_cache.shape[1], block_table.shape[1])
+    with torch.cuda.device(dev):
+        st = lib.cmp_kv_append(_ptr(k), _ptr(v), _ptr(norm_weight), None if rope is None else ctypes.byref(rope), eps,
+                               _ptr(block_table), _ptr(cu_seqlens), _ptr(start_pos), dt, _ptr(k_cache),
+                               _ptr(v_cache), _handle(stream, dev), ctypes.byref(dims))
+    if st != CMP_OK:
+        raise CmpError(st, "cmp_kv_append")
+    return k_cache, v_cache
+
+
+def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos=None, *, scale: Optional[float] = None,
+                    max_len: Optional[int] = None, window: Optional[int] = None, key_block: int = 1,
+                    key_stride: int = 1, out=None, lse=None, return_lse: bool = False, workspace=None, stream=None):
+    """Attention of the call's tokens over their sequences' cached keys (see
+    cmp_paged_attention in include/cmp.h); returns ``out``, or ``(out, lse)`` with
+    ``return_lse`` or a given ``lse``.
+
+    q [T, Hq, D] fp16 / bf16, last two dimensions dense; caches [block_num, page_size, Hk,
+    D] (page_size a multiple of 16); block_table int32 [B, pages]; cu_seqlens int32 [B+1];
+    start_pos int32 [B] or None (all 0): the position of each sequence's first token.
+    ``scale`` defaults to 1 / sqrt(D); ``max_len`` is the most tokens any sequence of the
+    call has (default T: give it, so that decoding is known as such); ``window`` the
+    keys a token sees at most; ``key_block`` / ``key_stride`` describe caches of compressed
+    rows. ``workspace``: a CUDA tensor of at least ``paged_attention_workspace`` bytes
+    (allocated per call by default)."""
+    import torch
+    dt = _dtype16(q, "q")
+    dev = q.device
+    if q.dim() != 3:
+        raise ValueError("q must be [T, Hq, D]")
+    T, Hq, D = q.shape
+    qs = _check_tokens(q, "q", q.dtype, (T, Hq, D), dev)
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be [block_num, page_size, Hk, D]")
+    Hk = k_cache.shape[2]
+    _check_cache(k_cache, v_cache, q.dtype, Hk, D, dev)
+    B = _check_sequences(block_table, cu_seqlens, start_pos, dev)
+    if max_len is not None and max_len < 1:
+        raise ValueError("max_len must be at least 1")
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1")
+    if scale is None:
+        scale = D ** -0.5
+    dims = cmp_attn_dims(B, T, Hq, Hk, D, qs, k_cache.shape[0], k_cache.shape[1], block_table.shape[1], max_len or 0)
+    need = int(lib.cmp_paged_attention_workspace(ctypes.byref(dims)))
+    handle = _handle(stream, dev)
+
+    def allocate():
+        return (torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out,
+                torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None and return_lse else lse,
+                torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace)
+
+    if stream is None:
+        out, lse, workspace = allocate()
+    else:  # memory that belongs to the stream the call runs on
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, dev)):
+            out, lse, workspace = allocate()
+    _check(out, "out", q.dtype, 3, dev)
+    if tuple(out.shape) != (T, Hq, D):
+        raise ValueError(f"out must be [{T}, {Hq}, {D}]")
+    if lse is not None:
+        _check(lse, "lse", torch.float32, 2, dev)
+        if tuple(lse.shape) != (T, Hq):
+            raise ValueError(f"lse must be [{T}, {Hq}]")
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of q")
+    with torch.cuda.device(dev):
+        st = lib.cmp_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(cu_seqlens),
+                                     _ptr(start_pos), scale, window or 0, key_block, key_stride, dt, _ptr(out),
+                                     _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), handle,
+                                     ctypes.byref(dims))
+    if st != CMP_OK:
+        raise CmpError(st, "cmp_paged_attention")
+    return out if lse is None else (out, lse)
+
+
+def paged_attention_workspace(T: int, Hq: int, Hk: int, D: int, max_len: Optional[int] = None) -> int:
+    """Bytes of ``workspace`` a ``paged_attention`` call of these sizes needs."""
+    d = cmp_attn_dims(1, T, Hq, Hk, D, Hq * D, 1, 16, 1, max_len or 0)
+    return int(lib.cmp_paged_attention_workspace(ctypes.byref(d)))
 
 
 def debug_check_tables(kv_block_table, state_block_table, cu_seqlens, start_pos, ratio: int,

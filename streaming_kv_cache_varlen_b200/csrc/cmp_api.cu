@@ -8,9 +8,15 @@
 #include <utility>
 #include <vector>
 
+#include <cmath>
+
+#include "cmp_attn.cuh"
 #include "cmp_internal.cuh"
 
 namespace cmp {
+cudaError_t launch_qk_norm_rope(const QkNormParams& p, cudaStream_t s, int sms);
+cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t s, int sms);
+cudaError_t kv_take_error(unsigned* word);
 cudaError_t launch_proj_tc(const Params& p, cudaStream_t s);
 cudaError_t launch_proj_decode(const Params& p, cudaStream_t s);
 bool proj_tc_supported(const Params& p);
@@ -240,6 +246,73 @@ int check_dims(const cmp_dims* d) {
   if (d->block_size < 1 || d->block_size > 1024) return CMP_ERR_INVALID;
   if (d->block_num < 1 || d->table_stride < 1) return CMP_ERR_INVALID;
   return CMP_OK;
+}
+
+// ---- paged cache operators -----------------------------------------------------
+
+// Devices on which an operator with a device-wide error word has run.
+std::atomic<uint64_t> g_word_devices{0};
+
+void note_word_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64)
+    g_word_devices.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+}
+
+bool in(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+bool valid_head_dim(int64_t D) { return in(D, 16, 256) && D % 16 == 0; }
+bool valid_dtype(int32_t t) { return t == CMP_NSA_FP16 || t == CMP_NSA_BF16; }
+// tokens of `heads` dense heads, `stride` elements apart
+bool valid_stride(int64_t stride, int64_t heads, int64_t D) {
+  return stride % 8 == 0 && in(stride, heads * D, int64_t(1) << 40);
+}
+
+int check_rope(const cmp_rope* r, int64_t D, cmp::RopeTable* o) {
+  *o = cmp::RopeTable{};
+  if (!r || r->dim == 0) return CMP_OK;
+  if (!in(r->dim, 16, D) || r->dim % 16) return CMP_ERR_INVALID;
+  if ((r->pairs != CMP_ROPE_INTERLEAVED && r->pairs != CMP_ROPE_HALVES) ||
+      (r->dtype != CMP_ROPE_F32 && r->dtype != CMP_ROPE_BF16))
+    return CMP_ERR_UNSUPPORTED;
+  if (!r->sin || !r->cos) return CMP_ERR_NULLPTR;
+  if (!aligned(r->sin, 16) || !aligned(r->cos, 16)) return CMP_ERR_INVALID;
+  o->sin = r->sin;
+  o->cos = r->cos;
+  o->dim = r->dim;
+  o->f32 = r->dtype == CMP_ROPE_F32;
+  o->halves = r->pairs == CMP_ROPE_HALVES;
+  return CMP_OK;
+}
+
+int check_attn_dims(const cmp_attn_dims* d) {
+  if (!d) return CMP_ERR_NULLPTR;
+  if (!in(d->B, 0, INT32_MAX - 1) || !in(d->T, 0, INT32_MAX - 1) || !in(d->Hq, 1, 1024) || !in(d->Hk, 1, 256) ||
+      d->Hq % d->Hk || d->Hq / d->Hk > 128 || !valid_head_dim(d->D) || d->T * d->Hq > INT32_MAX ||
+      !valid_stride(d->q_stride, d->Hq, d->D) || !in(d->page_size, 16, 1024) || d->page_size % 16 ||
+      !in(d->block_num, 1, INT32_MAX / d->page_size) || !in(d->table_stride, 1, INT32_MAX) ||
+      !in(d->max_len, 0, INT32_MAX) || (d->B == 0 && d->T != 0))
+    return CMP_ERR_INVALID;
+  return CMP_OK;
+}
+
+// How a call of paged attention runs, from its host-known sizes.
+struct AttnPath {
+  int m, ctas;  // rows per item; CTAs
+  size_t part, ml, desc, total;
+};
+
+AttnPath attn_path(const cmp_attn_dims& d) {
+  AttnPath a{};
+  cmp::AttnParams p{};
+  p.D = (int)d.D;
+  a.m = cmp::kAttnDecodeRows;
+  a.ctas = cmp::attn_decode_ctas(p, sm_count_cached());
+  const size_t slots = (size_t)a.ctas * 2 * a.m;
+  a.part = 0;
+  a.ml = a.part + slots * cmp::attn_padded((int)d.D) * sizeof(float);
+  a.desc = a.ml + slots * 2 * sizeof(float);
+  a.total = a.desc + (size_t)a.ctas * 2 * sizeof(int4);
+  return a;
 }
 
 // Returned by run_path when the device refused a launch form before anything
@@ -512,6 +585,162 @@ int cmp_nsa_compress(const void* input, const void* weight, const int32_t* slot_
   return CMP_OK;
 }
 
+int cmp_qk_norm_rope(const void* q, const void* k, const void* q_weight, const void* k_weight, const cmp_rope* rope,
+                     float eps, int32_t dtype, void* q_out, void* k_out, void* stream, const cmp_qk_dims* dims) {
+  if (!dims) return CMP_ERR_NULLPTR;
+  if (!valid_dtype(dtype)) return CMP_ERR_UNSUPPORTED;
+  const cmp_qk_dims& d = *dims;
+  const bool keys = d.Hk > 0;
+  if (!in(d.T, 0, INT32_MAX - 1) || !in(d.Hq, 1, 1024) || !in(d.Hk, 0, 1024) || !valid_head_dim(d.D) ||
+      !valid_stride(d.q_stride, d.Hq, d.D) || !valid_stride(d.q_out_stride, d.Hq, d.D) ||
+      (keys && (!valid_stride(d.k_stride, d.Hk, d.D) || !valid_stride(d.k_out_stride, d.Hk, d.D))) ||
+      !(eps >= 0.f) || std::isinf(eps))
+    return CMP_ERR_INVALID;
+  if (d.T == 0) return CMP_OK;
+  cmp::QkNormParams p{};
+  const int rc = check_rope(rope, d.D, &p.rope);
+  if (rc != CMP_OK) return rc;
+  if (!q || !q_weight || !q_out || (keys && (!k || !k_weight || !k_out))) return CMP_ERR_NULLPTR;
+  if (!aligned(q, 16) || !aligned(q_weight, 16) || !aligned(q_out, 16) ||
+      (keys && (!aligned(k, 16) || !aligned(k_weight, 16) || !aligned(k_out, 16))) ||
+      (q == q_out && d.q_stride != d.q_out_stride) || (keys && k == k_out && d.k_stride != d.k_out_stride))
+    return CMP_ERR_INVALID;
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.q_weight = static_cast<const uint16_t*>(q_weight);
+  p.k_weight = static_cast<const uint16_t*>(k_weight);
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.T = d.T;
+  p.q_stride = d.q_stride;
+  p.k_stride = d.k_stride;
+  p.qo_stride = d.q_out_stride;
+  p.ko_stride = d.k_out_stride;
+  p.Hq = (int)d.Hq;
+  p.Hk = (int)d.Hk;
+  p.D = (int)d.D;
+  p.bf16 = dtype == CMP_NSA_BF16 ? 1 : 0;
+  p.eps = eps;
+  p.inv_d = 1.f / (float)d.D;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launch(CMP_KERNEL_QK_NORM_ROPE, s, [&] { return cmp::launch_qk_norm_rope(p, s, sm_count_cached()); }) ==
+                 cudaSuccess
+             ? CMP_OK
+             : CMP_ERR_CUDA;
+}
+
+int cmp_kv_append(const void* k, const void* v, const void* norm_weight, const cmp_rope* rope, float eps,
+                  const int32_t* block_table, const int32_t* cu_seqlens, const int32_t* start_pos, int32_t dtype,
+                  void* k_cache, void* v_cache, void* stream, const cmp_kv_dims* dims) {
+  if (!dims) return CMP_ERR_NULLPTR;
+  if (!valid_dtype(dtype)) return CMP_ERR_UNSUPPORTED;
+  const cmp_kv_dims& d = *dims;
+  if (!in(d.B, 0, INT32_MAX - 1) || !in(d.T, 0, INT32_MAX - 1) || !in(d.Hk, 1, 256) || !valid_head_dim(d.D) ||
+      !valid_stride(d.k_stride, d.Hk, d.D) || !valid_stride(d.v_stride, d.Hk, d.D) || !in(d.page_size, 1, 1024) ||
+      !in(d.block_num, 1, INT32_MAX / d.page_size) || !in(d.table_stride, 1, INT32_MAX) || (d.B == 0 && d.T != 0) ||
+      !(eps >= 0.f) || std::isinf(eps))
+    return CMP_ERR_INVALID;
+  if (d.B == 0 || d.T == 0) return CMP_OK;
+  cmp::KvAppendParams p{};
+  const int rc = check_rope(rope, d.D, &p.rope);
+  if (rc != CMP_OK) return rc;
+  if (!k || !v || !block_table || !cu_seqlens || !k_cache || !v_cache) return CMP_ERR_NULLPTR;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(norm_weight, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(start_pos, 4))
+    return CMP_ERR_INVALID;
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.norm_weight = static_cast<const uint16_t*>(norm_weight);
+  p.table = block_table;
+  p.cu = cu_seqlens;
+  p.start_pos = start_pos;
+  p.k_cache = static_cast<uint16_t*>(k_cache);
+  p.v_cache = static_cast<uint16_t*>(v_cache);
+  p.T = d.T;
+  p.k_stride = d.k_stride;
+  p.v_stride = d.v_stride;
+  p.table_stride = d.table_stride;
+  p.block_num = d.block_num;
+  p.B = (int)d.B;
+  p.Hk = (int)d.Hk;
+  p.D = (int)d.D;
+  p.page = (int)d.page_size;
+  p.bf16 = dtype == CMP_NSA_BF16 ? 1 : 0;
+  p.eps = eps;
+  p.inv_d = 1.f / (float)d.D;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  note_word_device();
+  return launch(CMP_KERNEL_KV_APPEND, s, [&] { return cmp::launch_kv_append(p, s, sm_count_cached()); }) ==
+                 cudaSuccess
+             ? CMP_OK
+             : CMP_ERR_CUDA;
+}
+
+size_t cmp_paged_attention_workspace(const cmp_attn_dims* dims) {
+  if (check_attn_dims(dims) != CMP_OK) return 0;
+  return attn_path(*dims).total;
+}
+
+int cmp_paged_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                        const int32_t* cu_seqlens, const int32_t* start_pos, float scale, int64_t window,
+                        int64_t key_block, int64_t key_stride, int32_t dtype, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream, const cmp_attn_dims* dims) {
+  if (!dims) return CMP_ERR_NULLPTR;
+  if (!valid_dtype(dtype)) return CMP_ERR_UNSUPPORTED;
+  const int rc = check_attn_dims(dims);
+  if (rc != CMP_OK) return rc;
+  const cmp_attn_dims& d = *dims;
+  if (!(scale > 0.f) || std::isinf(scale) || !in(window, 0, INT32_MAX) || !in(key_block, 1, INT32_MAX) ||
+      !in(key_stride, 1, INT32_MAX))
+    return CMP_ERR_INVALID;
+  if (d.B == 0 || d.T == 0) return CMP_OK;
+  if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens || !out || !workspace) return CMP_ERR_NULLPTR;
+  const AttnPath a = attn_path(d);
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+      !aligned(block_table, 4) || !aligned(cu_seqlens, 4) || !aligned(start_pos, 4) || !aligned(workspace, 16) ||
+      workspace_bytes < a.total)
+    return CMP_ERR_INVALID;
+  cmp::AttnParams p{};
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.q = static_cast<const uint16_t*>(q);
+  p.table = block_table;
+  p.cu = cu_seqlens;
+  p.start_pos = start_pos;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.part = reinterpret_cast<float*>(ws + a.part);
+  p.part_ml = reinterpret_cast<float*>(ws + a.ml);
+  p.desc = reinterpret_cast<int4*>(ws + a.desc);
+  p.q_stride = d.q_stride;
+  p.table_stride = d.table_stride;
+  p.block_num = d.block_num;
+  p.B = (int)d.B;
+  p.T = (int)d.T;
+  p.Hq = (int)d.Hq;
+  p.Hk = (int)d.Hk;
+  p.G = (int)(d.Hq / d.Hk);
+  p.D = (int)d.D;
+  p.page = (int)d.page_size;
+  p.bf16 = dtype == CMP_NSA_BF16 ? 1 : 0;
+  p.key_block = (int)key_block;
+  p.key_stride = (int)key_stride;
+  p.window = (int)window;
+  p.max_len = (int)(d.max_len && d.max_len < d.T ? d.max_len : d.T);
+  p.run_shift = 4;
+  while (p.run_shift < 6 && p.page % (2 << p.run_shift) == 0) ++p.run_shift;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  CUtensorMap kmap, vmap;
+  if (!cmp::attn_cache_map(&kmap, k_cache, p) || !cmp::attn_cache_map(&vmap, v_cache, p)) return CMP_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  note_word_device();
+  if (launch(CMP_KERNEL_ATTN_DECODE, s, [&] { return cmp::launch_attn_decode(p, kmap, vmap, s, a.ctas); }) !=
+      cudaSuccess)
+    return CMP_ERR_CUDA;
+  if (launch(CMP_KERNEL_ATTN_COMBINE, s, [&] { return cmp::launch_attn_combine(p, a.m, a.ctas, s); }) != cudaSuccess)
+    return CMP_ERR_CUDA;
+  return CMP_OK;
+}
+
 int cmp_debug_unreachable_barrier(int launches) {
   if (launches < 0) return -1;
   return g_unreachable_barrier.exchange(launches);
@@ -547,6 +776,13 @@ int cmp_get_error(void* stream) {
   unsigned na = 0;  // the allocation-free entry point's calls on this device
   if (cmp::noalloc_take_error(dev, &na) != CMP_OK) return CMP_ERR_CUDA;
   word |= na;
+  if (dev < 64 && (g_word_devices.load(std::memory_order_relaxed) >> dev & 1)) {  // the paged cache operators' words
+    for (auto* take : {cmp::kv_take_error, cmp::attn_decode_take_error}) {
+      unsigned v = 0;
+      if (take(&v) != cudaSuccess) return CMP_ERR_CUDA;
+      word |= v;
+    }
+  }
   if (word & cmp::kErrTimeout) return CMP_ERR_TIMEOUT;
   if (word & cmp::kErrIndex) return CMP_ERR_DEVICE_INDEX;
   return CMP_OK;
@@ -569,7 +805,9 @@ const char* cmp_kernel_name(int kernel) {
   static const char* names[CMP_KERNEL_COUNT] = {"sched",         "proj_tcgen05",  "proj_mma_sync",
                                                 "proj_decode",   "pool_epilogue", "fused_tcgen05",
                                                 "finish",        "decode_fused",  "decode_cp",
-                                                "nsa_compress",  "nsa_scan"};
+                                                "nsa_compress",  "nsa_scan",
+                                                "qk_norm_rope",  "kv_append",     "attn_decode",
+                                                "attn_combine"};
   return (kernel >= 0 && kernel < CMP_KERNEL_COUNT) ? names[kernel] : nullptr;
 }
 

@@ -1,0 +1,295 @@
+// Attention of a chunk of new tokens over a paged cache: what its kernels share
+// (the call's parameters, the division of the work, the joining of split rows).
+//
+// A token at position p sees the first n(p) keys of its sequence,
+//   n(p) = 0 if p + 1 < key_block, else (p + 1 - key_block) / key_stride + 1,
+// (key j stands for positions j*key_stride .. j*key_stride + key_block - 1), of
+// those the last `window` if there is a window. The query heads of one key head
+// are rows of the same tile: row r of a (sequence, key head) is token r / G, query
+// head r % G of the group of G = Hq / Hk.
+//
+// Work: an item is a tile of M rows of one (sequence, key head); its units are
+// the tiles of KT keys that any of its rows sees (an item without keys has one
+// empty unit, so that its rows are written). All units of a call form a line,
+// sequence by sequence, head by head, row tile by row tile, and CTA c takes the
+// c-th of equal parts of it, whatever the lengths are. An item that a part's end
+// cuts is finished in pieces: each piece leaves its fp32 accumulator and its
+// softmax statistics in the workspace (a CTA leaves at most two: slot 0 for an
+// item begun by an earlier CTA, slot 1 for one that it begins and does not end),
+// and attn_combine_kernel joins them in the order of the keys.
+#pragma once
+
+#include "cmp_internal.cuh"
+#include "cmp_sm100.cuh"
+
+#include <cuda_fp16.h>
+
+namespace cmp {
+
+struct AttnParams {
+  const uint16_t* q;         // token t at q + t * q_stride, its [Hq, D] dense
+  const int32_t* table;      // [B, table_stride]
+  const int32_t* cu;         // [B + 1]
+  const int32_t* start_pos;  // [B] or null
+  uint16_t* out;             // [T, Hq, D]
+  float* lse;                // [T, Hq] or null
+  float* part;               // workspace: accumulators of cut items [ctas][2][M][DP]
+  float* part_ml;            // [ctas][2][M][2]: running maximum (log2 units), sum
+  int4* desc;                // [ctas][2]: the item a CTA begins and does not end
+  int64_t q_stride, table_stride, block_num;
+  int B, T, Hq, Hk, G, D, page, bf16;
+  int key_block, key_stride, window;  // window 0: none
+  int max_len;
+  int run_shift;      // keys per TMA box: 1 << run_shift, a divisor of the page
+  float scale_log2;   // scale * log2(e)
+};
+
+struct AttnSeq {
+  int t0, len, start;  // first row of q, tokens, position of the first one
+  bool bad;
+};
+
+// Sequence b, with length 0 if its entries are not usable (bad is set then).
+__device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
+  AttnSeq s;
+  const int c = __ldg(p.cu + b), e = __ldg(p.cu + b + 1);
+  s.start = p.start_pos ? __ldg(p.start_pos + b) : 0;
+  s.t0 = c;
+  s.len = e - c;
+  s.bad = c < 0 || e < c || e > p.T || s.start < 0 || (b == 0 && c != 0) || (int64_t)s.start + (e - c) > INT32_MAX ||
+          s.len > p.max_len;
+  if (s.bad) s.len = 0;
+  return s;
+}
+
+__device__ __forceinline__ int attn_keys(const AttnParams& p, int p1) {  // p1 = position + 1
+  if (p.key_stride == 1) return max(p1 - p.key_block + 1, 0);
+  return p1 < p.key_block ? 0 : (p1 - p.key_block) / p.key_stride + 1;
+}
+
+// Keys [lo, hi) that any of the rows [row0, row0 + rows) sees; hi <= lo: none.
+__device__ __forceinline__ void attn_range(const AttnParams& p, const AttnSeq& s, int row0, int rows, int& lo,
+                                           int& hi) {
+  hi = attn_keys(p, s.start + (row0 + rows - 1) / p.G + 1);
+  lo = p.window ? max(0, attn_keys(p, s.start + row0 / p.G + 1) - p.window) : 0;
+}
+
+// The visible keys [lo, hi) of one row.
+__device__ __forceinline__ void attn_row_range(const AttnParams& p, const AttnSeq& s, int row, int& lo, int& hi) {
+  hi = attn_keys(p, s.start + row / p.G + 1);
+  lo = p.window ? max(0, hi - p.window) : 0;
+}
+
+// One piece of an item: tiles [j0, j1) of its [T0, T1).
+struct AttnPiece {
+  AttnSeq s;
+  int b, h;        // sequence, key head
+  int row0, rows;  // rows of the (sequence, key head)
+  int lo, hi;      // keys any row sees (hi <= lo: none)
+  int T0, T1, j0, j1;
+  __device__ __forceinline__ bool whole() const { return j0 == T0 && j1 == T1; }
+};
+
+// Rows per tile: M, or for a tile that is loaded as whole tokens the largest
+// multiple of G up to M.
+template <int KT>
+__device__ __forceinline__ void attn_tiles(int lo, int hi, int& T0, int& T1) {
+  T0 = hi > lo ? lo / KT : 0;
+  T1 = hi > lo ? (hi + KT - 1) / KT : 1;
+}
+
+// A CTA's way along its part of the line. `m` rows per item.
+template <int KT>
+struct AttnWalk {
+  const AttnParams& p;
+  int m;
+  int64_t left;  // units still to do
+  int b, h, qt, off;
+  int nq;
+  AttnSeq s;
+  __device__ __forceinline__ AttnWalk(const AttnParams& p_, int m_) : p(p_), m(m_) {}
+  __device__ __forceinline__ void open() {
+    s = attn_seq(p, b);
+    nq = (int)(((int64_t)s.len * p.G + m - 1) / m);
+  }
+  __device__ __forceinline__ void begin(int64_t units, int b_, int h_, int qt_, int off_) {
+    left = units;
+    b = b_;
+    h = h_;
+    qt = qt_;
+    off = off_;
+    if (left > 0) open();
+  }
+  __device__ __forceinline__ bool next(AttnPiece& o) {
+    if (left <= 0) return false;
+    while (qt >= nq) {
+      qt = 0;
+      if (++h >= p.Hk) {
+        h = 0;
+        if (++b >= p.B) return false;
+        open();
+      }
+      if (nq == 0) h = p.Hk - 1;
+    }
+    o.s = s;
+    o.b = b;
+    o.h = h;
+    o.row0 = qt * m;
+    o.rows = min(m, s.len * p.G - o.row0);
+    attn_range(p, s, o.row0, o.rows, o.lo, o.hi);
+    attn_tiles<KT>(o.lo, o.hi, o.T0, o.T1);
+    const int n = o.T1 - o.T0;
+    const int take = (int)min(left, (int64_t)(n - off));
+    o.j0 = o.T0 + off;
+    o.j1 = o.j0 + take;
+    left -= take;
+    off += take;
+    if (off >= n) {
+      off = 0;
+      ++qt;
+    }
+    return true;
+  }
+};
+
+// Where a CTA's part begins, found by all NT threads of the CTA together.
+struct AttnStart {
+  int64_t share, units;  // units per CTA; this CTA's units
+  int b, h, qt, off;
+};
+
+// Units of one key head of sequence s.
+template <int KT>
+__device__ __forceinline__ int64_t attn_head_units(const AttnParams& p, const AttnSeq& s, int m) {
+  int64_t n = 0;
+  for (int64_t r = 0; r < (int64_t)s.len * p.G; r += m) {
+    int lo, hi, T0, T1;
+    attn_range(p, s, (int)r, (int)min((int64_t)m, (int64_t)s.len * p.G - r), lo, hi);
+    attn_tiles<KT>(lo, hi, T0, T1);
+    n += T1 - T0;
+  }
+  return n;
+}
+
+// Every thread sums its run of consecutive sequences, the block scans the sums,
+// and the thread whose run holds the part's first unit walks to it. *err gets
+// kErrIndex from CTA 0 if a sequence is not usable. Ends with __syncthreads.
+template <int KT, int NT>
+__device__ __forceinline__ void attn_plan(const AttnParams& p, int m, AttnStart* st, int64_t* warp_sum,
+                                          unsigned* err) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.B + NT - 1) / NT;
+  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+  int64_t sum = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const AttnSeq s = attn_seq(p, b);
+    bad |= s.bad;
+    sum += attn_head_units<KT>(p, s, m) * p.Hk;
+  }
+  if (bad && blockIdx.x == 0) atomicOr(err, kErrIndex);
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  if (tid == 0) st->units = 0;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < (NT + 31) / 32; ++w) {
+    if (w < warp) base += warp_sum[w];
+    total += warp_sum[w];
+  }
+  base += inc - sum;
+  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  int64_t u = (int64_t)blockIdx.x * share;
+  if (u < total && u >= base && u < base + sum) {
+    st->share = share;
+    st->units = min(share, total - u);
+    u -= base;
+    for (int b = b0; b < b1; ++b) {
+      const AttnSeq s = attn_seq(p, b);
+      const int64_t hu = attn_head_units<KT>(p, s, m);
+      if (u >= hu * p.Hk) {
+        u -= hu * p.Hk;
+        continue;
+      }
+      st->b = b;
+      st->h = (int)(u / hu);
+      u %= hu;
+      int qt = 0;
+      for (;; ++qt) {
+        int lo, hi, T0, T1;
+        const int r = qt * m;
+        attn_range(p, s, r, min(m, s.len * p.G - r), lo, hi);
+        attn_tiles<KT>(lo, hi, T0, T1);
+        if (u < T1 - T0) break;
+        u -= T1 - T0;
+      }
+      st->qt = qt;
+      st->off = (int)u;
+      break;
+    }
+  }
+  __syncthreads();
+}
+
+// The CTA's note on the item that it begins and leaves to later CTAs: the last
+// of them (0: there is none; CTA 0 is never one), the rows and where they go.
+__device__ __forceinline__ void attn_write_desc(const AttnParams& p, int cta, int last_cta, const AttnPiece* o) {
+  p.desc[2 * cta] = o ? make_int4(last_cta, o->rows, o->s.t0, o->row0) : make_int4(0, 0, 0, 0);
+  if (o) p.desc[2 * cta + 1] = make_int4(o->h, 0, 0, 0);
+}
+
+// The last CTA of the item of a piece that its CTA does not end: `rest` tiles
+// follow, the next CTAs do `share` each.
+__device__ __forceinline__ int attn_last_cta(int cta, int64_t share, const AttnPiece& o) {
+  return cta + (int)((o.T1 - o.j1 + share - 1) / share);
+}
+
+// Row r of a piece's item -> the row of out / lse ([T * Hq]).
+__device__ __forceinline__ int64_t attn_out_row(const AttnParams& p, int t0, int h, int r) {
+  return (int64_t)(t0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
+
+// log of sum exp from the running maximum (log2 units) and the sum.
+__device__ __forceinline__ float attn_lse(float m, float l) {
+  return l > 0.f ? fmaf(m, 0.69314718055994531f, logf(l)) : neg_inf();
+}
+
+// Accumulator columns of a head of D channels: a multiple of 64.
+inline int attn_padded(int D) { return (D + 63) / 64 * 64; }
+
+// Host: the cache as a 3-D tensor (d, key head, row) with boxes of 64 channels of
+// one head over 1 << run_shift rows, landing 128-byte swizzled.
+bool attn_cache_map(CUtensorMap* m, const void* cache, const AttnParams& p);
+
+cudaError_t launch_attn_decode(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s,
+                               int ctas);
+int attn_decode_ctas(const AttnParams& p, int sms);
+constexpr int kAttnDecodeRows = 16;  // rows per item of the decode kernel
+cudaError_t launch_attn_combine(const AttnParams& p, int m, int ctas, cudaStream_t s);
+cudaError_t attn_decode_take_error(unsigned* word);
+
+}  // namespace cmp

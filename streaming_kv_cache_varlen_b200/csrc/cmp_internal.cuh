@@ -157,6 +157,58 @@ struct NsaParams {
   int64_t tokens, table_stride, result_len;
 };
 
+// The position rotation's tables: row t holds dim columns for token t.
+struct RopeTable {
+  const void* sin;  // [T, dim] float32 (f32) or bf16
+  const void* cos;
+  int dim;     // rotated channels (the last ones of a head); 0: no rotation
+  int f32;
+  int halves;  // pairs (j, dim/2 + j) instead of (2j, 2j + 1)
+};
+
+// One qk_norm_rope call, device pointers (16-bit elements).
+struct QkNormParams {
+  const uint16_t* q;         // token t at q + t * q_stride, its [Hq, D] dense
+  const uint16_t* k;         // likewise (Hk = 0: none)
+  const uint16_t* q_weight;  // [D]
+  const uint16_t* k_weight;  // [D]
+  uint16_t* q_out;
+  uint16_t* k_out;
+  RopeTable rope;
+  int64_t T, q_stride, k_stride, qo_stride, ko_stride;
+  int Hq, Hk, D, bf16;
+  float eps, inv_d;
+};
+
+// One kv_append call, device pointers (16-bit elements).
+struct KvAppendParams {
+  const uint16_t* k;            // token t at k + t * k_stride, its [Hk, D] dense
+  const uint16_t* v;
+  const uint16_t* norm_weight;  // [D] or null
+  RopeTable rope;
+  const int32_t* table;      // [B, table_stride]
+  const int32_t* cu;         // [B + 1]
+  const int32_t* start_pos;  // [B] or null
+  uint16_t* k_cache;         // [block_num, page, Hk, D]
+  uint16_t* v_cache;
+  int64_t T, k_stride, v_stride, table_stride, block_num;
+  int B, Hk, D, page, bf16;
+  float eps, inv_d;
+};
+
+// Reads and clears a __device__ error word on the current device (the caller has
+// synchronised the streams whose calls it wants covered).
+template <class W>
+inline cudaError_t take_symbol_word(W& symbol, unsigned* word) {
+  *word = 0;
+  unsigned v = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, symbol, sizeof(v));
+  const unsigned zero = 0;
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(symbol, &zero, sizeof(zero));
+  *word = v;
+  return e;
+}
+
 // Kernel launchers (each file defines its own).
 cudaError_t launch_sched(const Params& p, cudaStream_t s);
 cudaError_t launch_proj_mma(const Params& p, cudaStream_t s);

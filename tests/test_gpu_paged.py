@@ -1,0 +1,370 @@
+"""The paged cache operators on a B200 against their oracle (oracle/paged.py):
+qk_norm_rope, kv_append and paged_attention, each alone and as they run together."""
+
+import numpy as np
+import pytest
+
+from oracle import paged as oracle
+from oracle.nsa import to_f64
+from tests.paged_helpers import assert_attention, assert_normed, b16, bits, dev
+from workloads import make_paged_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- qk_norm_rope ------------------------------------------------------------
+
+
+def norm_case(lib, i, pairs, *, packed=False, tables=None, eps=1e-6, in_place=False):
+    import torch
+    T, Hq, D = i.q.shape
+    Hk = i.k.shape[1]
+    q, k = b16(i.q, i.dtype), b16(i.k, i.dtype)
+    if packed:  # parts of one projection's output
+        qkv = torch.cat([q, k, b16(i.v, i.dtype)], 1)
+        q, k = qkv[:, :Hq], qkv[:, Hq:Hq + Hk]
+        before = bits(qkv[:, Hq + Hk:])
+    sin, cos = dev(i.sin), dev(i.cos)
+    if tables == "bf16" and sin is not None:
+        sin, cos = sin.bfloat16(), cos.bfloat16()
+    w = b16(i.weight, i.dtype)
+    w2 = w.flip(0).contiguous()
+    qo, ko = lib.qk_norm_rope(q, k, w, w2, sin=sin, cos=cos, rope_pairs=pairs, eps=eps,
+                              q_out=q if in_place else None, k_out=k if in_place else None)
+    assert lib.get_error() == 0
+    s64 = None if sin is None else sin.float().cpu().numpy()
+    c64 = None if cos is None else cos.float().cpu().numpy()
+    wv = to_f64(i.weight, i.dtype)
+    for got, src, wt in ((qo, i.q, wv), (ko, i.k, wv[::-1])):
+        ref, mag = oracle.norm_rope(to_f64(src, i.dtype), wt, s64, c64, pairs, eps)
+        assert_normed(bits(got), ref, mag, i.dtype)
+    if packed:
+        assert np.array_equal(bits(qkv[:, Hq + Hk:]), before)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("pairs", ["interleaved", "halves"])
+@pytest.mark.parametrize("T,Hq,Hk,D,rope", [(1, 1, 1, 16, 16), (5, 3, 1, 64, 32), (33, 7, 5, 80, 48),
+                                            (17, 32, 8, 128, 128), (3, 40, 24, 192, 64), (9, 5, 2, 256, 256),
+                                            (7, 4, 2, 144, 0), (700, 9, 3, 32, 16)])
+def test_norm_shapes(lib, dtype, pairs, T, Hq, Hk, D, rope):
+    i = make_paged_inputs(seed=T + D, lens=[T], ctx=[3], Hq=Hq, Hk=Hk, D=D, page=16, dtype=dtype, rope=rope)
+    norm_case(lib, i, pairs)
+
+
+@pytest.mark.parametrize("pairs", ["interleaved", "halves"])
+@pytest.mark.parametrize("tables", ["f32", "bf16"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_norm_of_a_packed_projection(lib, pairs, tables, in_place):
+    i = make_paged_inputs(seed=5, lens=[40], ctx=[100000], Hq=12, Hk=4, D=128, page=16, rope=64)
+    norm_case(lib, i, pairs, packed=True, tables=tables, in_place=in_place)
+
+
+def test_norm_queries_only_and_zero_rows(lib):
+    import torch
+    q = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    out, none = lib.qk_norm_rope(q, None, w, eps=1e-6)
+    assert none is None and torch.equal(out, q)
+    big = torch.full((1, 1, 64), 3e38, dtype=torch.bfloat16, device="cuda")  # the sum of squares overflows
+    out, _ = lib.qk_norm_rope(big, None, w)
+    assert not torch.isnan(out).any()
+    out, _ = lib.qk_norm_rope(q[:0], None, w)
+    assert out.shape == (0, 2, 64)
+
+
+# ---- kv_append ---------------------------------------------------------------
+
+
+def append_case(lib, i, pairs="interleaved", norm=True, stream=None):
+    import torch
+    kc, vc = b16(i.k_cache, i.dtype), b16(i.v_cache, i.dtype)
+    w = b16(i.weight, i.dtype) if norm else None
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    lib.kv_append(b16(i.k, i.dtype), b16(i.v, i.dtype), kc, vc, dev(i.block_table), dev(i.cu_seqlens),
+                  dev(i.start_pos), norm_weight=w, sin=dev(i.sin), cos=dev(i.cos), rope_pairs=pairs, stream=stream)
+    torch.cuda.synchronize()
+    assert lib.get_error() == 0
+    D = i.k.shape[2]
+    ref, mag = oracle.norm_rope(to_f64(i.k, i.dtype), to_f64(i.weight, i.dtype) if norm else None, i.sin, i.cos, pairs,
+                                1e-6)
+    at = oracle.cache_rows(i.block_table, i.cu_seqlens, i.start_pos, i.page)
+    tok, row = np.asarray(at, dtype=np.int64).reshape(-1, 2).T
+    gk, gv = bits(kc).reshape(-1, *i.k.shape[1:]), bits(vc).reshape(-1, *i.k.shape[1:])
+    if i.sin is None and not norm:
+        assert np.array_equal(gk[row], i.k[tok])
+    else:
+        assert_normed(gk[row], ref[tok], mag[tok], i.dtype)
+    assert np.array_equal(gv[row], i.v[tok])
+    left = np.ones(gk.shape[0], dtype=bool)
+    left[row] = False
+    assert np.array_equal(gk[left], i.k_cache.reshape(-1, *i.k.shape[1:])[left])
+    assert np.array_equal(gv[left], i.v_cache.reshape(-1, *i.k.shape[1:])[left])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("pairs", ["interleaved", "halves"])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("lens,ctx,Hk,D,page,rope", [
+    ([1], [0], 1, 16, 16, 16),
+    ([1] * 40, list(range(0, 400, 10)), 8, 128, 64, 64),
+    ([0, 5, 0, 0, 129, 1, 0], [7, 0, 9, 0, 63, 16, 5], 3, 80, 16, 0),
+    ([300, 17], [1000, 31], 5, 192, 128, 192),
+    ([33, 64, 2], [0, 1, 2], 2, 256, 1, 32),
+    ([50], [5], 24, 64, 100, 48),
+])
+def test_append_shapes(lib, dtype, pairs, norm, lens, ctx, Hk, D, page, rope):
+    i = make_paged_inputs(seed=sum(lens) + D, lens=lens, ctx=ctx, Hq=1, Hk=Hk, D=D, page=page, dtype=dtype, rope=rope)
+    append_case(lib, i, pairs, norm)
+
+
+def test_append_many_sequences_and_padding(lib):
+    """2000 sequences (three rounds of the sequence search), most of them empty, and
+    tokens behind the last one, which are not stored."""
+    rng = np.random.default_rng(0)
+    lens = [int(x) for x in rng.integers(0, 3, 2000)]
+    i = make_paged_inputs(seed=2, lens=lens, ctx=[int(x) for x in rng.integers(0, 40, 2000)], Hq=1, Hk=2, D=32, page=16,
+                          rope=32, extra_tokens=77)
+    append_case(lib, i)
+
+
+def test_append_bad_entries_are_reported(lib):
+    import torch
+    i = make_paged_inputs(seed=3, lens=[20, 20, 4], ctx=[0, 0, 0], Hq=1, Hk=2, D=64, page=16)
+    tbl = i.block_table.copy()
+    tbl[0, 1] = -1
+    tbl[1, 0] = i.k_cache.shape[0]
+    kc, vc = b16(i.k_cache, i.dtype), b16(i.v_cache, i.dtype)
+    args = (b16(i.k, i.dtype), b16(i.v, i.dtype), kc, vc)
+    lib.kv_append(*args, dev(tbl), dev(i.cu_seqlens), dev(i.start_pos))
+    assert lib.get_error() == 5 and lib.get_error() == 0
+    gk = bits(kc).reshape(-1, 2, 64)
+    stored = 0
+    for t, row in oracle.cache_rows(tbl, i.cu_seqlens, i.start_pos, 16):
+        if 0 <= row < gk.shape[0]:
+            assert np.array_equal(gk[row], i.k[t])
+            stored += 1
+    assert stored == 16 + 4 + 4
+    for cu, sp in (([0, 20, 10, 44], [0, 0, 0]), ([0, 20, 40, 60], [0, 0, 0]), ([3, 20, 40, 44], [0, 0, 0]),
+                   ([0, 20, 40, 44], [0, -3, 0]), ([0, 20, 40, 44], [0, 0, 2 ** 31 - 2])):
+        lib.kv_append(*args, dev(i.block_table), dev(np.asarray(cu, np.int32)), dev(np.asarray(sp, np.int32)))
+        assert lib.get_error() == 5, (cu, sp)
+    torch.cuda.synchronize()
+
+
+def test_append_on_another_stream(lib):
+    import torch
+    i = make_paged_inputs(seed=4, lens=[100, 3], ctx=[5, 6], Hq=1, Hk=4, D=128, page=32, rope=64)
+    append_case(lib, i, stream=torch.cuda.Stream())
+
+
+# ---- paged_attention ---------------------------------------------------------
+
+
+def attn_inputs(seed, lens, ctx, Hq, Hk, D, page, dtype="bf16", key_block=1, key_stride=1, **kw):
+    rows = [oracle.visible(c + n - 1, key_block, key_stride)[1] if n else 0 for n, c in zip(lens, ctx)]
+    return make_paged_inputs(seed=seed, lens=lens, ctx=ctx, Hq=Hq, Hk=Hk, D=D, page=page, dtype=dtype, rows=rows, **kw)
+
+
+def attn_case(lib, i, *, key_block=1, key_stride=1, window=0, scale=None, stale=None, max_len="exact", stream=None):
+    """``stale``: what every cache row that no token of the call sees holds (a number, NaN included)."""
+    import torch
+    D = i.q.shape[2]
+    scale = D ** -0.5 if scale is None else scale
+    kc, vc = i.k_cache.copy(), i.v_cache.copy()
+    tbl = i.block_table.copy()
+    if stale is not None:
+        seen = np.zeros(kc.shape[0] * i.page, dtype=bool)
+        for b in range(len(i.start_pos)):
+            n = int(i.cu_seqlens[b + 1] - i.cu_seqlens[b])
+            span = [oracle.visible(int(i.start_pos[b]) + t, key_block, key_stride, window) for t in range(n)]
+            keys = {j for lo, hi in span for j in (range(lo, hi) if n <= 2 else ())}
+            if n > 2:
+                keys = range(min(s[0] for s in span), max(s[1] for s in span))
+            used = set()
+            for j in keys:
+                seen[int(tbl[b][j // i.page]) * i.page + j % i.page] = True
+                used.add(j // i.page)
+            for c in range(tbl.shape[1]):
+                if c not in used:
+                    tbl[b, c] = -1
+        fill = np.float16(stale).view(np.uint16) if i.dtype == "fp16" else (
+            np.uint16(0x7FC0) if np.isnan(stale) else np.uint16(np.float32(stale).view(np.uint32) >> 16))
+        kc.reshape(-1, *kc.shape[2:])[~seen] = fill
+        vc.reshape(-1, *vc.shape[2:])[~seen] = fill
+    lens = np.diff(i.cu_seqlens)
+    if max_len == "exact":
+        max_len = max(1, int(lens.max(initial=0)))
+    if stream is not None:
+        stream.wait_stream(torch.cuda.current_stream())
+    out = torch.full(i.q.shape, 7.0, dtype=torch.float16 if i.dtype == "fp16" else torch.bfloat16, device="cuda")
+    lse = torch.full(i.q.shape[:2], 7.0, device="cuda")
+    args = (b16(i.q, i.dtype), b16(kc, i.dtype), b16(vc, i.dtype), dev(tbl), dev(i.cu_seqlens), dev(i.start_pos))
+    torch.cuda.synchronize()
+    lib.paged_attention(*args, scale=scale, max_len=max_len, window=window or None, key_block=key_block,
+                        key_stride=key_stride, out=out, lse=lse, stream=stream)
+    torch.cuda.synchronize()
+    assert lib.get_error() == 0
+    res = oracle.paged_attention(to_f64(i.q, i.dtype), to_f64(i.k_cache, i.dtype), to_f64(i.v_cache, i.dtype),
+                                 i.block_table, i.cu_seqlens, i.start_pos, scale, key_block=key_block,
+                                 key_stride=key_stride, window=window)
+    assert_attention(bits(out), lse.cpu().numpy(), res, i.dtype)
+    assert torch.all(out[int(i.cu_seqlens[-1]):] == 7) and torch.all(lse[int(i.cu_seqlens[-1]):] == 7)
+    return out, lse, args
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [16, 64, 80, 128, 192, 256])
+@pytest.mark.parametrize("lens,ctx,Hq,Hk,page", [
+    ([1], [0], 1, 1, 16),                                   # one key
+    ([1, 1, 1], [63, 64, 200], 8, 2, 64),                   # a tile's last key, the next one's first
+    ([1] * 5, [0, 1, 500, 17, 1300], 12, 4, 16),            # ragged, cut items
+    ([2, 0, 5], [40, 3, 333], 6, 2, 48),                    # a few tokens each, pages of 48
+])
+def test_decode(lib, dtype, D, lens, ctx, Hq, Hk, page):
+    attn_case(lib, attn_inputs(D + len(lens), lens, ctx, Hq, Hk, D, page, dtype))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [48, 64, 128, 192, 256])
+@pytest.mark.parametrize("lens,ctx,Hq,Hk,page", [
+    ([70], [0], 2, 1, 32),                                  # a prompt's first chunk
+    ([129, 1, 0, 40], [127, 300, 9, 0], 4, 4, 128),         # chunks next to decoding
+    ([37, 90], [600, 2], 14, 2, 16),                        # seven heads per key head
+    ([33], [5], 48, 2, 64),                                 # 24 heads per key head
+])
+def test_chunks(lib, dtype, D, lens, ctx, Hq, Hk, page):
+    attn_case(lib, attn_inputs(D + sum(lens), lens, ctx, Hq, Hk, D, page, dtype))
+
+
+@pytest.mark.parametrize("lens,ctx", [([1, 1, 1], [0, 100, 700]), ([50, 9, 260], [0, 31, 300])])
+@pytest.mark.parametrize("kb,ks,window", [(1, 1, 5), (1, 1, 100), (4, 4, 0), (32, 16, 0), (32, 16, 3), (1, 1, 4000),
+                                          (128, 128, 0)])
+def test_windows_and_compressed_rows(lib, lens, ctx, kb, ks, window):
+    """Rows that see nothing (tokens before the first compressed row) are 0 with lse -inf."""
+    i = attn_inputs(kb + window, lens, ctx, 8, 2, 64, 32, key_block=kb, key_stride=ks)
+    attn_case(lib, i, key_block=kb, key_stride=ks, window=window)
+
+
+@pytest.mark.parametrize("stale", [float("nan"), float("inf"), -3e38])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("lens,ctx,window,D", [([1, 1], [100, 1023], 0, 128), ([1, 2], [100, 300], 40, 64),
+                                               ([90, 200], [11, 77], 0, 128), ([60, 33], [200, 700], 50, 192)])
+def test_unseen_rows_may_hold_anything(lib, stale, dtype, lens, ctx, window, D):
+    """Rows behind a sequence's end, before its window, and blocks that are not its own
+    (their table entries are -1) do not reach the outputs."""
+    if dtype == "fp16" and abs(stale) < 1e39 and not np.isinf(stale):
+        stale = -65504.0
+    attn_case(lib, attn_inputs(9, lens, ctx, 8, 2, D, 64, dtype), window=window, stale=stale)
+
+
+@pytest.mark.parametrize("Hq,Hk", [(128, 1), (16, 1), (17, 1), (64, 64), (15, 5), (36, 12)])
+def test_head_layouts(lib, Hq, Hk):
+    attn_case(lib, attn_inputs(Hq, [1, 3], [70, 200], Hq, Hk, 64, 16))
+
+
+def test_max_len_unknown_and_padding(lib):
+    i = attn_inputs(1, [3, 1, 1], [60, 400, 0], 8, 2, 128, 64, extra_tokens=9)
+    a, la, _ = attn_case(lib, i, max_len=None)
+    attn_case(lib, i, max_len=3)
+
+
+def test_strided_queries(lib):
+    import torch
+    i = attn_inputs(2, [40, 1], [100, 500], 8, 2, 128, 64)
+    out, lse, args = attn_case(lib, i)
+    qkv = torch.randn(41, 12, 128, device="cuda").to(torch.bfloat16)
+    qkv[:, :8] = args[0]
+    out2, lse2 = lib.paged_attention(qkv[:, :8], *args[1:], max_len=40, return_lse=True)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lens,ctx", [([1], [3000]), ([1, 1, 1], [0, 5000, 40]), ([200, 1], [900, 4000])])
+def test_long_context(lib, lens, ctx):
+    attn_case(lib, attn_inputs(3, lens, ctx, 8, 2, 128, 64))
+
+
+def test_large_scores(lib):
+    """Scores far apart (weights under- and overflowing a fixed reference)."""
+    attn_case(lib, attn_inputs(4, [1, 80], [700, 300], 4, 2, 128, 32), scale=4.0)
+
+
+def test_growing_scores(lib):
+    """The running maximum grows by much from tile to tile, and falls behind."""
+    from workloads.synth import bf16_bits
+    i = attn_inputs(5, [1, 70], [1500, 600], 4, 1, 64, 64)
+    g = np.ones(i.k_cache.shape[:2], np.float32)
+    for b in range(2):
+        n = int(i.start_pos[b] + i.cu_seqlens[b + 1] - i.cu_seqlens[b])
+        for j in range(n):
+            g[i.block_table[b][j // 64], j % 64] = 0.2 + 6.0 * j / n if b == 0 else 6.0 * (n - j) / n
+    i.k_cache = bf16_bits((to_f64(i.k_cache, "bf16") * g[..., None, None]).astype(np.float32))
+    attn_case(lib, i)
+
+
+def test_repeat_is_bit_identical(lib):
+    import torch
+    i = attn_inputs(6, [1] * 7 + [100], [10, 500, 2000, 3, 0, 77, 900, 60], 8, 2, 128, 64)
+    out, lse, args = attn_case(lib, i)
+    for _ in range(5):
+        o, l = lib.paged_attention(*args, max_len=100, return_lse=True)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_two_streams_at_once(lib):
+    import torch
+    i = attn_inputs(7, [1] * 6, [1000, 500, 2000, 3, 0, 77], 8, 2, 128, 64)
+    j = attn_inputs(8, [130], [600], 8, 2, 128, 64)
+    oi, li, ai = attn_case(lib, i)
+    oj, lj, aj = attn_case(lib, j)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    res = []
+    for _ in range(10):
+        res.append((lib.paged_attention(*ai, max_len=1, return_lse=True, stream=s1),
+                    lib.paged_attention(*aj, max_len=130, return_lse=True, stream=s2)))
+    torch.cuda.synchronize()
+    for (a, b) in res:
+        assert torch.equal(a[0], oi) and torch.equal(a[1], li) and torch.equal(b[0], oj) and torch.equal(b[1], lj)
+    assert lib.get_error() == 0
+
+
+def test_bad_entries_are_reported(lib):
+    import torch
+    i = attn_inputs(9, [1, 1, 20], [100, 50, 30], 4, 2, 64, 16)
+    out, lse, args = attn_case(lib, i)
+    tbl = i.block_table.copy()
+    tbl[0, 2] = i.k_cache.shape[0] + 9
+    o, l = lib.paged_attention(*args[:3], dev(tbl), *args[4:], max_len=20, return_lse=True)
+    assert lib.get_error() == 5 and lib.get_error() == 0
+    assert torch.equal(o[1:], out[1:]) and torch.isfinite(o.float()).all()
+    for cu, sp, ml in (([0, 1, 0, 22], [100, 50, 30], 22), ([0, 1, 2, 23], [100, 50, 30], 20),
+                       ([0, 1, 2, 22], [100, -1, 30], 20), ([0, 1, 2, 22], [100, 50, 30], 19),
+                       ([0, 1, 2, 22], [2 ** 31 - 1, 50, 30], 20), ([1, 1, 2, 22], [100, 50, 30], 20)):
+        lib.paged_attention(*args[:4], dev(np.asarray(cu, np.int32)), dev(np.asarray(sp, np.int32)), max_len=ml)
+        assert lib.get_error() == 5, (cu, sp, ml)
+    torch.cuda.synchronize()
+
+
+def test_captured_and_replayed(lib):
+    """A decode step of all three operators in a graph, replayed after its inputs moved on."""
+    import torch
+    i = attn_inputs(10, [1, 1], [90, 300], 8, 2, 128, 64, rope=64)
+    q, k, v = b16(i.q, "bf16"), b16(i.k, "bf16"), b16(i.v, "bf16")
+    kc, vc, tbl, cu = b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16"), dev(i.block_table), dev(i.cu_seqlens)
+    sp, w, sin, cos = dev(i.start_pos), b16(i.weight, "bf16"), dev(i.sin), dev(i.cos)
+
+    def step():
+        qn, _ = lib.qk_norm_rope(q, None, w, sin=sin, cos=cos)
+        lib.kv_append(k, v, kc, vc, tbl, cu, sp, norm_weight=w, sin=sin, cos=cos)
+        return lib.paged_attention(qn, kc, vc, tbl, cu, sp, max_len=1, return_lse=True)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = step()
+    for shift in (0, -1, -30):
+        sp.copy_(dev(i.start_pos) + shift)
+        g.replay()
+        eager = step()
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+    assert lib.get_error() == 0

@@ -19,3 +19,4 @@ from .synth import (  # noqa: F401
     sylvester,
 )
 from .nsa import NsaInputs, make_nsa_inputs  # noqa: F401,E402
+from .paged import PagedInputs, make_paged_inputs  # noqa: F401,E402
