@@ -429,7 +429,8 @@ enum {
   CMP_KERNEL_KV_APPEND = 12,
   CMP_KERNEL_ATTN_DECODE = 13,  /* paged attention, few rows per key head */
   CMP_KERNEL_ATTN_COMBINE = 14, /* paged attention: joins rows that were cut between CTAs */
-  CMP_KERNEL_COUNT = 15
+  CMP_KERNEL_ATTN_CHUNK = 15,   /* paged attention, many rows per key head */
+  CMP_KERNEL_COUNT = 16
 };
 
 /* Name of a kernel id (NULL if out of range). */

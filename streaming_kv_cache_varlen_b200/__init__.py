@@ -23,7 +23,7 @@ STATUS = {0: "CMP_OK", 1: "CMP_ERR_NULLPTR", 2: "CMP_ERR_INVALID", 3: "CMP_ERR_U
           4: "CMP_ERR_CUDA", 5: "CMP_ERR_DEVICE_INDEX", 6: "CMP_ERR_TIMEOUT"}
 KERNELS = ("sched", "proj_tcgen05", "proj_mma_sync", "proj_decode", "pool_epilogue",
            "fused_tcgen05", "finish", "decode_fused", "decode_cp", "nsa_compress", "nsa_scan",
-           "qk_norm_rope", "kv_append", "attn_decode", "attn_combine")
+           "qk_norm_rope", "kv_append", "attn_decode", "attn_combine", "attn_chunk")
 
 
 class CmpError(RuntimeError):

@@ -297,7 +297,9 @@ int check_attn_dims(const cmp_attn_dims* d) {
 
 // How a call of paged attention runs, from its host-known sizes.
 struct AttnPath {
+  bool chunk;   // 128-row MMA tiles
   int m, ctas;  // rows per item; CTAs
+  int key_tile;
   size_t part, ml, desc, total;
 };
 
@@ -305,8 +307,11 @@ AttnPath attn_path(const cmp_attn_dims& d) {
   AttnPath a{};
   cmp::AttnParams p{};
   p.D = (int)d.D;
-  a.m = cmp::kAttnDecodeRows;
-  a.ctas = cmp::attn_decode_ctas(p, sm_count_cached());
+  const int64_t len = d.max_len && d.max_len < d.T ? d.max_len : d.T;
+  a.chunk = len * (d.Hq / d.Hk) > cmp::kAttnDecodeRows;
+  a.m = a.chunk ? cmp::attn_chunk_rows(p.D) : cmp::kAttnDecodeRows;
+  a.ctas = a.chunk ? sm_count_cached() : cmp::attn_decode_ctas(p, sm_count_cached());
+  a.key_tile = a.chunk ? cmp::attn_chunk_key_tile(p.D) : 64;
   const size_t slots = (size_t)a.ctas * 2 * a.m;
   a.part = 0;
   a.ml = a.part + slots * cmp::attn_padded((int)d.D) * sizeof(float);
@@ -727,15 +732,16 @@ int cmp_paged_attention(const void* q, const void* k_cache, const void* v_cache,
   p.window = (int)window;
   p.max_len = (int)(d.max_len && d.max_len < d.T ? d.max_len : d.T);
   p.run_shift = 4;
-  while (p.run_shift < 6 && p.page % (2 << p.run_shift) == 0) ++p.run_shift;
+  while ((1 << p.run_shift) < a.key_tile && p.page % (2 << p.run_shift) == 0) ++p.run_shift;
   p.scale_log2 = scale * 1.4426950408889634f;
   CUtensorMap kmap, vmap;
   if (!cmp::attn_cache_map(&kmap, k_cache, p) || !cmp::attn_cache_map(&vmap, v_cache, p)) return CMP_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   note_word_device();
-  if (launch(CMP_KERNEL_ATTN_DECODE, s, [&] { return cmp::launch_attn_decode(p, kmap, vmap, s, a.ctas); }) !=
-      cudaSuccess)
-    return CMP_ERR_CUDA;
+  const cudaError_t e =
+      a.chunk ? launch(CMP_KERNEL_ATTN_CHUNK, s, [&] { return cmp::launch_attn_chunk(p, kmap, vmap, s, a.ctas); })
+              : launch(CMP_KERNEL_ATTN_DECODE, s, [&] { return cmp::launch_attn_decode(p, kmap, vmap, s, a.ctas); });
+  if (e != cudaSuccess) return CMP_ERR_CUDA;
   if (launch(CMP_KERNEL_ATTN_COMBINE, s, [&] { return cmp::launch_attn_combine(p, a.m, a.ctas, s); }) != cudaSuccess)
     return CMP_ERR_CUDA;
   return CMP_OK;
@@ -777,7 +783,7 @@ int cmp_get_error(void* stream) {
   if (cmp::noalloc_take_error(dev, &na) != CMP_OK) return CMP_ERR_CUDA;
   word |= na;
   if (dev < 64 && (g_word_devices.load(std::memory_order_relaxed) >> dev & 1)) {  // the paged cache operators' words
-    for (auto* take : {cmp::kv_take_error, cmp::attn_decode_take_error}) {
+    for (auto* take : {cmp::kv_take_error, cmp::attn_decode_take_error, cmp::attn_chunk_take_error}) {
       unsigned v = 0;
       if (take(&v) != cudaSuccess) return CMP_ERR_CUDA;
       word |= v;
@@ -807,7 +813,7 @@ const char* cmp_kernel_name(int kernel) {
                                                 "finish",        "decode_fused",  "decode_cp",
                                                 "nsa_compress",  "nsa_scan",
                                                 "qk_norm_rope",  "kv_append",     "attn_decode",
-                                                "attn_combine"};
+                                                "attn_combine",  "attn_chunk"};
   return (kernel >= 0 && kernel < CMP_KERNEL_COUNT) ? names[kernel] : nullptr;
 }
 

@@ -158,21 +158,41 @@ struct AttnStart {
   int b, h, qt, off;
 };
 
-// Units of one key head of sequence s.
+// Units of row tile qt of one key head of sequence s.
 template <int KT>
-__device__ __forceinline__ int64_t attn_head_units(const AttnParams& p, const AttnSeq& s, int m) {
+__device__ __forceinline__ int attn_tile_units(const AttnParams& p, const AttnSeq& s, int m, int qt) {
+  int lo, hi, T0, T1;
+  const int r = qt * m;
+  attn_range(p, s, r, min(m, s.len * p.G - r), lo, hi);
+  attn_tiles<KT>(lo, hi, T0, T1);
+  return T1 - T0;
+}
+
+// Units of one key head of each lane's sequence, by the whole warp: sequences of
+// few row tiles by their own lane, the others by all lanes one after another.
+template <int KT>
+__device__ __forceinline__ int64_t attn_head_units(const AttnParams& p, const AttnSeq& s, int m, int lane) {
+  const int nq = (int)(((int64_t)s.len * p.G + m - 1) / m);
   int64_t n = 0;
-  for (int64_t r = 0; r < (int64_t)s.len * p.G; r += m) {
-    int lo, hi, T0, T1;
-    attn_range(p, s, (int)r, (int)min((int64_t)m, (int64_t)s.len * p.G - r), lo, hi);
-    attn_tiles<KT>(lo, hi, T0, T1);
-    n += T1 - T0;
+  if (nq <= 4)
+    for (int qt = 0; qt < nq; ++qt) n += attn_tile_units<KT>(p, s, m, qt);
+  for (unsigned big = __ballot_sync(0xffffffffu, nq > 4); big; big &= big - 1) {
+    const int src = __ffs(big) - 1;
+    AttnSeq t;
+    t.len = __shfl_sync(0xffffffffu, s.len, src);
+    t.start = __shfl_sync(0xffffffffu, s.start, src);
+    const int tq = __shfl_sync(0xffffffffu, nq, src);
+    int64_t part = 0;
+    for (int qt = lane; qt < tq; qt += 32) part += attn_tile_units<KT>(p, t, m, qt);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == src) n = part;
   }
   return n;
 }
 
 // Every thread sums its run of consecutive sequences, the block scans the sums,
-// and the thread whose run holds the part's first unit walks to it. *err gets
+// and the warp whose run holds the part's first unit walks to it. *err gets
 // kErrIndex from CTA 0 if a sequence is not usable. Ends with __syncthreads.
 template <int KT, int NT>
 __device__ __forceinline__ void attn_plan(const AttnParams& p, int m, AttnStart* st, int64_t* warp_sum,
@@ -182,10 +202,13 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int m, AttnStart*
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
   int64_t sum = 0;
   bool bad = false;
-  for (int b = b0; b < b1; ++b) {
-    const AttnSeq s = attn_seq(p, b);
+  for (int i = 0; i < per; ++i) {  // lanes of a warp together
+    AttnSeq s;
+    s.t0 = s.len = s.start = 0;
+    s.bad = false;
+    if (b0 + i < b1) s = attn_seq(p, b0 + i);
     bad |= s.bad;
-    sum += attn_head_units<KT>(p, s, m) * p.Hk;
+    sum += attn_head_units<KT>(p, s, m, lane) * p.Hk;
   }
   if (bad && blockIdx.x == 0) atomicOr(err, kErrIndex);
   int64_t inc = sum;
@@ -206,31 +229,47 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int m, AttnStart*
   base += inc - sum;
   const int64_t share = (total + gridDim.x - 1) / gridDim.x;
   int64_t u = (int64_t)blockIdx.x * share;
-  if (u < total && u >= base && u < base + sum) {
-    st->share = share;
-    st->units = min(share, total - u);
-    u -= base;
-    for (int b = b0; b < b1; ++b) {
+  // the warp whose run holds unit u walks to it, 32 row tiles at a time
+  const unsigned owner = __ballot_sync(0xffffffffu, u < total && u >= base && u < base + sum);
+  if (owner) {
+    const int src = __ffs(owner) - 1;
+    const int sb0 = __shfl_sync(0xffffffffu, b0, src), sb1 = __shfl_sync(0xffffffffu, b1, src);
+    int64_t v = u - __shfl_sync(0xffffffffu, base, src);
+    for (int b = sb0; b < sb1; ++b) {
       const AttnSeq s = attn_seq(p, b);
-      const int64_t hu = attn_head_units<KT>(p, s, m);
-      if (u >= hu * p.Hk) {
-        u -= hu * p.Hk;
+      const int nq = (int)(((int64_t)s.len * p.G + m - 1) / m);
+      int64_t hu = 0;
+      for (int qt = lane; qt < nq; qt += 32) hu += attn_tile_units<KT>(p, s, m, qt);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) hu += __shfl_xor_sync(0xffffffffu, hu, o);
+      if (v >= hu * p.Hk) {
+        v -= hu * p.Hk;
         continue;
       }
-      st->b = b;
-      st->h = (int)(u / hu);
-      u %= hu;
-      int qt = 0;
-      for (;; ++qt) {
-        int lo, hi, T0, T1;
-        const int r = qt * m;
-        attn_range(p, s, r, min(m, s.len * p.G - r), lo, hi);
-        attn_tiles<KT>(lo, hi, T0, T1);
-        if (u < T1 - T0) break;
-        u -= T1 - T0;
+      const int h = (int)(v / hu);
+      v -= h * hu;
+      for (int qt0 = 0;; qt0 += 32) {
+        const int n = qt0 + lane < nq ? attn_tile_units<KT>(p, s, m, qt0 + lane) : 0;
+        int64_t c = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t t = __shfl_up_sync(0xffffffffu, c, o);
+          if (lane >= o) c += t;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, v < c);
+        if (past) {
+          if (lane == __ffs(past) - 1) {
+            st->share = share;
+            st->units = min(share, total - u);
+            st->b = b;
+            st->h = h;
+            st->qt = qt0 + lane;
+            st->off = (int)(v - (c - n));
+          }
+          break;
+        }
+        v -= __shfl_sync(0xffffffffu, c, 31);
       }
-      st->qt = qt;
-      st->off = (int)u;
       break;
     }
   }
@@ -275,7 +314,7 @@ __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u)
 
 // log of sum exp from the running maximum (log2 units) and the sum.
 __device__ __forceinline__ float attn_lse(float m, float l) {
-  return l > 0.f ? fmaf(m, 0.69314718055994531f, logf(l)) : neg_inf();
+  return l == 0.f ? neg_inf() : fmaf(m, 0.69314718055994531f, logf(l));  // a NaN stays one
 }
 
 // Accumulator columns of a head of D channels: a multiple of 64.
@@ -289,6 +328,12 @@ cudaError_t launch_attn_decode(const AttnParams& p, const CUtensorMap& k, const 
                                int ctas);
 int attn_decode_ctas(const AttnParams& p, int sms);
 constexpr int kAttnDecodeRows = 16;  // rows per item of the decode kernel
+// Chunks: 128-row MMA tiles, one CTA per SM.
+int attn_chunk_rows(int D);      // rows per item
+int attn_chunk_key_tile(int D);  // keys per tile
+cudaError_t launch_attn_chunk(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s,
+                              int ctas);
+cudaError_t attn_chunk_take_error(unsigned* word);
 cudaError_t launch_attn_combine(const AttnParams& p, int m, int ctas, cudaStream_t s);
 cudaError_t attn_decode_take_error(unsigned* word);
 

@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) attn_combine_kernel(const AttnParams
         acc[v].y = fmaf(x.y, w, acc[v].y);
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t row = attn_out_row(p, t0, h, row0 + r);
 #pragma unroll
     for (int v = 0; v < V / 2; ++v) {
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) attn_combine_kernel(const AttnParams
 
 template <bool BF16, int DP>
 cudaError_t run(const AttnParams& p, int m, int ctas, cudaStream_t s) {
-  const dim3 grid((unsigned)ctas, (unsigned)((m + kWarps - 1) / kWarps));
+  const dim3 grid((unsigned)ctas, (unsigned)((m + 4 * kWarps - 1) / (4 * kWarps)));
   return launch_chained(attn_combine_kernel<BF16, DP>, grid, dim3(kThreads), 0, s, 1, p, m);
 }
 

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
       const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
       if (whole) {
         const int64_t row = attn_out_row(p, o.s.t0, o.h, o.row0 + r);
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         if (c < p.D) {
           uint4 v;
           v.x = pack2<BF16>(a.x * inv, a.y * inv);
