@@ -41,6 +41,7 @@ struct AttnParams {
   int key_block, key_stride, window;  // window 0: none
   int max_len;
   int run_shift;      // keys per TMA box: 1 << run_shift, a divisor of the page
+  uint32_t inv_g;     // ceil(2^23 / G), see attn_div_g
   float scale_log2;   // scale * log2(e)
 };
 
@@ -292,6 +293,12 @@ __device__ __forceinline__ int attn_last_cta(int cta, int64_t share, const AttnP
 // Row r of a piece's item -> the row of out / lse ([T * Hq]).
 __device__ __forceinline__ int64_t attn_out_row(const AttnParams& p, int t0, int h, int r) {
   return (int64_t)(t0 + r / p.G) * p.Hq + h * p.G + r % p.G;
+}
+
+// x / G for x < 384 (a row of a tile of 256 behind a remainder below G <= 128):
+// inv_g = (2^23 + e) / G with e < G, and x e <= 383 * 127 < 2^23 / G.
+__device__ __forceinline__ int attn_div_g(const AttnParams& p, int x) {
+  return (int)(((uint32_t)x * p.inv_g) >> 23);
 }
 
 __device__ __forceinline__ float ex2(float x) {
