@@ -733,7 +733,9 @@ int cmp_paged_attention(const void* q, const void* k_cache, const void* v_cache,
   p.max_len = (int)(d.max_len && d.max_len < d.T ? d.max_len : d.T);
   p.run_shift = 4;
   while ((1 << p.run_shift) < a.key_tile && p.page % (2 << p.run_shift) == 0) ++p.run_shift;
-  p.inv_g = ((1u << 23) + (uint32_t)p.G - 1) / (uint32_t)p.G;
+  p.div_g = cmp::make_fast_div(p.G);
+  p.div_stride = cmp::make_fast_div(p.key_stride);
+  p.div_page = cmp::make_fast_div(p.page);
   p.scale_log2 = scale * 1.4426950408889634f;
   CUtensorMap kmap, vmap;
   if (!cmp::attn_cache_map(&kmap, k_cache, p) || !cmp::attn_cache_map(&vmap, v_cache, p)) return CMP_ERR_CUDA;

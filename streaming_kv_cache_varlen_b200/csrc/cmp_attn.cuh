@@ -9,8 +9,9 @@
 // head r % G of the group of G = Hq / Hk.
 //
 // Work: an item is a tile of M rows of one (sequence, key head); its units are
-// the tiles of KT keys that any of its rows sees (an item without keys has one
-// empty unit, so that its rows are written). All units of a call form a line,
+// kItemCost for loading its queries and storing its rows, then the tiles of KT keys
+// that any of its rows sees (an item without keys has one empty tile, so that its
+// rows are written). All units of a call form a line,
 // sequence by sequence, head by head, row tile by row tile, and CTA c takes the
 // c-th of equal parts of it, whatever the lengths are. An item that a part's end
 // cuts is finished in pieces: each piece leaves its fp32 accumulator and its
@@ -26,6 +27,27 @@
 
 namespace cmp {
 
+// Division by a number that the host knows: n / d for 0 <= n < 2^31, 1 <= d < 2^31.
+// With s = ceil(log2 d) and mul = ceil(2^(31+s) / d) = (2^(31+s) + e) / d, 0 <= e < d <= 2^s,
+// the excess n e / (d 2^(31+s)) stays below 1 / d, so the floor is exact.
+struct FastDiv {
+  uint32_t mul;
+  int shift;
+  int d;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
+#endif
+};
+inline FastDiv make_fast_div(int d) {
+  FastDiv f;
+  int s = 0;
+  while (s < 31 && (int64_t(1) << s) < d) ++s;
+  f.shift = 31 + s;
+  f.mul = (uint32_t)((((uint64_t)1 << (31 + s)) + (uint32_t)d - 1) / (uint32_t)d);
+  f.d = d;
+  return f;
+}
+
 struct AttnParams {
   const uint16_t* q;         // token t at q + t * q_stride, its [Hq, D] dense
   const int32_t* table;      // [B, table_stride]
@@ -38,10 +60,10 @@ struct AttnParams {
   int4* desc;                // [ctas][2]: the item a CTA begins and does not end
   int64_t q_stride, table_stride, block_num;
   int B, T, Hq, Hk, G, D, page, bf16;
-  int key_block, key_stride, window;  // window 0: none
+  FastDiv div_g, div_stride, div_page;  // by G, key_stride, page
+  int key_block, key_stride, window;    // window 0: none
   int max_len;
   int run_shift;      // keys per TMA box: 1 << run_shift, a divisor of the page
-  uint32_t inv_g;     // ceil(2^23 / G), see attn_div_g
   float scale_log2;   // scale * log2(e)
 };
 
@@ -65,19 +87,19 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
 
 __device__ __forceinline__ int attn_keys(const AttnParams& p, int p1) {  // p1 = position + 1
   if (p.key_stride == 1) return max(p1 - p.key_block + 1, 0);
-  return p1 < p.key_block ? 0 : (p1 - p.key_block) / p.key_stride + 1;
+  return p1 < p.key_block ? 0 : p.div_stride.div(p1 - p.key_block) + 1;
 }
 
 // Keys [lo, hi) that any of the rows [row0, row0 + rows) sees; hi <= lo: none.
 __device__ __forceinline__ void attn_range(const AttnParams& p, const AttnSeq& s, int row0, int rows, int& lo,
                                            int& hi) {
-  hi = attn_keys(p, s.start + (row0 + rows - 1) / p.G + 1);
-  lo = p.window ? max(0, attn_keys(p, s.start + row0 / p.G + 1) - p.window) : 0;
+  hi = attn_keys(p, s.start + p.div_g.div(row0 + rows - 1) + 1);
+  lo = p.window ? max(0, attn_keys(p, s.start + p.div_g.div(row0) + 1) - p.window) : 0;
 }
 
 // The visible keys [lo, hi) of one row.
 __device__ __forceinline__ void attn_row_range(const AttnParams& p, const AttnSeq& s, int row, int& lo, int& hi) {
-  hi = attn_keys(p, s.start + row / p.G + 1);
+  hi = attn_keys(p, s.start + p.div_g.div(row) + 1);
   lo = p.window ? max(0, hi - p.window) : 0;
 }
 
@@ -98,6 +120,12 @@ __device__ __forceinline__ void attn_tiles(int lo, int hi, int& T0, int& T1) {
   T0 = hi > lo ? lo / KT : 0;
   T1 = hi > lo ? (hi + KT - 1) / KT : 1;
 }
+
+// What an item costs beside its tiles, in tiles. Measured on items of one to three
+// tiles of the chunk kernel: 6 us each beside 2 us per tile; without it a batch that
+// mixes short and long contexts waits for the CTAs whose parts are all short items
+// (compressed rows of a prompt: 322 us).
+constexpr int kItemCost = 3;
 
 // A CTA's way along its part of the line. `m` rows per item.
 template <int KT>
@@ -122,34 +150,36 @@ struct AttnWalk {
     if (left > 0) open();
   }
   __device__ __forceinline__ bool next(AttnPiece& o) {
-    if (left <= 0) return false;
-    while (qt >= nq) {
-      qt = 0;
-      if (++h >= p.Hk) {
-        h = 0;
-        if (++b >= p.B) return false;
-        open();
+    while (left > 0) {
+      while (qt >= nq) {
+        qt = 0;
+        if (++h >= p.Hk) {
+          h = 0;
+          if (++b >= p.B) return false;
+          open();
+        }
+        if (nq == 0) h = p.Hk - 1;
       }
-      if (nq == 0) h = p.Hk - 1;
+      o.s = s;
+      o.b = b;
+      o.h = h;
+      o.row0 = qt * m;
+      o.rows = min(m, s.len * p.G - o.row0);
+      attn_range(p, s, o.row0, o.rows, o.lo, o.hi);
+      attn_tiles<KT>(o.lo, o.hi, o.T0, o.T1);
+      const int n = o.T1 - o.T0 + kItemCost;
+      const int take = (int)min(left, (int64_t)(n - off));
+      o.j0 = o.T0 + max(off - kItemCost, 0);
+      o.j1 = o.T0 + max(off + take - kItemCost, 0);
+      left -= take;
+      off += take;
+      if (off >= n) {
+        off = 0;
+        ++qt;
+      }
+      if (o.j1 > o.j0) return true;  // else the part ends before the item's first tile: the next CTA begins it
     }
-    o.s = s;
-    o.b = b;
-    o.h = h;
-    o.row0 = qt * m;
-    o.rows = min(m, s.len * p.G - o.row0);
-    attn_range(p, s, o.row0, o.rows, o.lo, o.hi);
-    attn_tiles<KT>(o.lo, o.hi, o.T0, o.T1);
-    const int n = o.T1 - o.T0;
-    const int take = (int)min(left, (int64_t)(n - off));
-    o.j0 = o.T0 + off;
-    o.j1 = o.j0 + take;
-    left -= take;
-    off += take;
-    if (off >= n) {
-      off = 0;
-      ++qt;
-    }
-    return true;
+    return false;
   }
 };
 
@@ -166,7 +196,7 @@ __device__ __forceinline__ int attn_tile_units(const AttnParams& p, const AttnSe
   const int r = qt * m;
   attn_range(p, s, r, min(m, s.len * p.G - r), lo, hi);
   attn_tiles<KT>(lo, hi, T0, T1);
-  return T1 - T0;
+  return T1 - T0 + kItemCost;
 }
 
 // Units of one key head of each lane's sequence, by the whole warp: sequences of
@@ -292,13 +322,8 @@ __device__ __forceinline__ int attn_last_cta(int cta, int64_t share, const AttnP
 
 // Row r of a piece's item -> the row of out / lse ([T * Hq]).
 __device__ __forceinline__ int64_t attn_out_row(const AttnParams& p, int t0, int h, int r) {
-  return (int64_t)(t0 + r / p.G) * p.Hq + h * p.G + r % p.G;
-}
-
-// x / G for x < 384 (a row of a tile of 256 behind a remainder below G <= 128):
-// inv_g = (2^23 + e) / G with e < G, and x e <= 383 * 127 < 2^23 / G.
-__device__ __forceinline__ int attn_div_g(const AttnParams& p, int x) {
-  return (int)(((uint32_t)x * p.inv_g) >> 23);
+  const int t = p.div_g.div(r);
+  return (int64_t)(t0 + t) * p.Hq + h * p.G + (r - t * p.G);
 }
 
 __device__ __forceinline__ float ex2(float x) {

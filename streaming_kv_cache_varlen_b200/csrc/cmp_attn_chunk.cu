@@ -18,6 +18,8 @@
 // common factor cancels in out and lse.
 #include "cmp_attn.cuh"
 
+#include <type_traits>
+
 namespace cmp {
 namespace {
 
@@ -27,6 +29,7 @@ constexpr int kThreads = 12 * 32;
 // (128 values), the other 4 give theirs up. 8 * 216 + 4 * 72 = 12 * 168, the launch's.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kPieces = 4;                // pieces the scheduler runs ahead
+constexpr int kPolyPairs = 6;             // of 16 pairs of weights, those that exp2_pair takes
 constexpr float kLazy = 8.f;              // log2 of the largest weight
 
 __device__ unsigned g_attn_err;
@@ -46,7 +49,7 @@ struct ChunkCfg {
 template <int DP>
 struct ChunkBars {
   uint64_t full[ChunkCfg<DP>::kStages], empty[ChunkCfg<DP>::kStages];
-  uint64_t q_ready[2], s_full[2], p_ready[2], o_full[2], last;
+  uint64_t q_ready[2], s_full[2], p_half[2], p_ready[2], o_full[2], last;
   uint64_t piece_full[kPieces], piece_empty[kPieces];
 };
 
@@ -58,7 +61,40 @@ struct ChunkPiece {
   bool valid;      // false: the CTA's part ends here
 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+// 2^x of two values below 2^7 without the special function unit: x = n + f with n
+// the nearest integer (adding 1.5 * 2^23 leaves n in the low bits of the sum), a
+// polynomial for 2^f on [-1/2, 1/2], n added to its exponent. The polynomial is the
+// degree-5 one of least maximal relative error, from a weighted least-squares fit
+// iterated on the error (Lawson); with its roundings it is off by at most 3.6 * 2^-24,
+// as ex2.approx (2^-22). Values below -127.5 give 0; not for NaN or infinities.
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t v) {
+  constexpr float kMagic = 12582912.f;
+  float a, b;
+  sm100::f2_unpack(v, a, b);
+  const uint64_t x = sm100::f2_pack(fmaxf(a, -128.f), fmaxf(b, -128.f));
+  const uint64_t t = sm100::f2_add(x, sm100::f2_pack(kMagic, kMagic));
+  const uint64_t n = sm100::f2_add(t, sm100::f2_pack(-kMagic, -kMagic));
+  const uint64_t f = sm100::f2_fma(n, sm100::f2_pack(-1.f, -1.f), x);
+  auto c = [](float k) { return sm100::f2_pack(k, k); };
+  uint64_t p = sm100::f2_fma(c(0x1.5c08e4p-10f), f, c(0x1.3d0c52p-7f));
+  p = sm100::f2_fma(p, f, c(0x1.c6b6e4p-5f));
+  p = sm100::f2_fma(p, f, c(0x1.ebf918p-3f));
+  p = sm100::f2_fma(p, f, c(0x1.62e428p-1f));
+  p = sm100::f2_fma(p, f, c(0x1.000002p+0f));
+  float pa, pb, ta, tb;
+  sm100::f2_unpack(p, pa, pb);
+  sm100::f2_unpack(t, ta, tb);
+  const int ra = max(__float_as_int(pa) + (int)(__float_as_uint(ta) << 23), 0);
+  const int rb = max(__float_as_int(pb) + (int)(__float_as_uint(tb) << 23), 0);
+  return sm100::f2_pack(__int_as_float(ra), __int_as_float(rb));
+}
+
+// The largest of three; NaN if one of them is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 
 template <bool BF16, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -87,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int w = 0; w < 2; ++w) {
       sm100::mbar_init(&bars.q_ready[w], 4);
       sm100::mbar_init(&bars.s_full[w], 1);
+      sm100::mbar_init(&bars.p_half[w], 4);
       sm100::mbar_init(&bars.p_ready[w], 4);
       sm100::mbar_init(&bars.o_full[w], 1);
     }
@@ -127,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool valid = walk.next(o);
           if (valid) {
             c.o = o;
-            c.last_cta = attn_last_cta(blockIdx.x, share, o);
-            c.tok0 = o.row0 / p.G;
+            if (o.j0 == o.T0 && !o.whole()) c.last_cta = attn_last_cta(blockIdx.x, share, o);
+            c.tok0 = p.div_g.div(o.row0);
             c.rem0 = o.row0 - c.tok0 * p.G;
           }
           c.valid = valid;
@@ -163,9 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool need = has && key < o.hi && key + (1 << run_shift) > o.lo;
           int row = no_row;
           if (need) {
-            const int pg = key / p.page;
+            const int pg = p.div_page.div(key);
             const int e = pg < p.table_stride ? __ldg(trow + pg) : -1;
-            if (e >= 0 && e < p.block_num) row = e * p.page + key % p.page;
+            if (e >= 0 && e < p.block_num) row = e * p.page + (key - pg * p.page);
             else atomicOr(&g_attn_err, kErrIndex);
           }
           const unsigned m = __ballot_sync(0xffffffffu, need);
@@ -188,75 +225,103 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!sm100::drain_armed(bars.full, C::kStages, armed) || !alive)
         if (lane == 0) atomicOr(&g_attn_err, kErrTimeout);
     } else if (warp == 8) {  // ---- products ----
-      if (lane == 0) {
-        constexpr uint32_t idesc_qk = sm100::idesc_16bit_f32(kRows, KT, BF16, false);
-        const uint32_t idesc_pv = sm100::idesc_16bit_f32(kRows, p.D, BF16, true);
-        const int ks = p.D / 16;
-        const uint32_t ring_a = sm100::smem_u32(ring), q_a = sm100::smem_u32(qs);
-        uint32_t nq = 0, np = 0;  // parities of the next Q and P tile, bit w: row tile w
-        int n = 0;                                // ring position of the item's first tile
-        bool ok = true;
-        auto take = [&](uint64_t* bar, uint32_t& parities, int w) {
-          ok = ok && sm100::mbar_wait(bar + w, (parities >> w) & 1u, &abort_flag);
-          parities ^= 1u << w;
-          sm100::tc_fence_after();
-        };
-        auto stage = [&](int i) {  // wait for ring position i
-          ok = ok && sm100::mbar_wait(&bars.full[i % C::kStages], (uint32_t)(i / C::kStages) & 1u, &abort_flag);
-          sm100::tc_fence_after();
-          return ring_a + (uint32_t)(i % C::kStages) * C::kTileBytes;
-        };
-        auto qk = [&](int w, uint32_t ka) {
-          const uint32_t qa = q_a + w * C::kQBytes;
-          for (int k = 0; k < ks; ++k)
-            sm100::mma_bf16(tmem + w * KT, sm100::sw128_kmajor_desc(qa + (k >> 2) * (kRows * 128) + (k & 3) * 32),
-                            sm100::sw128_kmajor_desc(ka + (k >> 2) * (KT * 128) + (k & 3) * 32), idesc_qk, k > 0);
-          sm100::mma_commit(&bars.s_full[w]);
-        };
-        auto pv = [&](int w, uint32_t va, bool first) {
-#pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            sm100::mma_ts(tmem + C::kTiles * KT + w * DP, tmem + w * KT + k * 8,
-                          sm100::sw128_mnmajor_desc(va + k * 2048, KT * 128), idesc_pv, !first || k > 0);
-        };
-        for (int pi = 0; ok; ++pi) {
-          const ChunkPiece* c = piece(pi);
-          ok = c != nullptr;
-          if (!ok || !c->valid) break;
-          const bool keys = c->o.hi > c->o.lo;
-          const int act = c->o.rows > kRows ? 2 : 1;
-          const int cnt = c->o.j1 - c->o.j0;
-          piece_done(pi);
-          if (!keys) continue;
-          uint32_t ka = stage(n);
-          for (int w = 0; w < act; ++w) {
-            take(bars.q_ready, nq, w);
-            if (ok) qk(w, ka);
-          }
-          if (ok) sm100::mma_commit(&bars.empty[n % C::kStages]);
-          for (int i = 0; ok && i < cnt; ++i, n += 2) {
-            const bool more = i + 1 < cnt;
-            const uint32_t va = stage(n + 1);
-            for (int w = 0; w < act; ++w) {
-              take(bars.p_ready, np, w);
-              if (!ok) break;
-              pv(w, va, i == 0);
-              if (more) {
-                if (w == 0) ka = stage(n + 2);
-                if (ok) qk(w, ka);
-              } else {
-                sm100::mma_commit(&bars.o_full[w]);
-              }
-            }
-            if (!ok) break;
-            sm100::mma_commit(&bars.empty[(n + 1) % C::kStages]);
-            if (more) sm100::mma_commit(&bars.empty[(n + 2) % C::kStages]);
-          }
+      // the whole warp keeps the loop (its values stay uniform), one lane issues
+      constexpr uint32_t idesc_qk = sm100::idesc_16bit_f32(kRows, KT, BF16, false);
+      const uint32_t idesc_pv = sm100::idesc_16bit_f32(kRows, p.D, BF16, true);
+      const int ks = p.D / 16;
+      const bool leader = sm100::elect_one();
+      const uint32_t q_lo = sm100::sw128_lo(sm100::smem_u32(qs), 16), k_lo = sm100::sw128_lo(sm100::smem_u32(ring), 16),
+                     v_lo = sm100::sw128_lo(sm100::smem_u32(ring), KT * 128);
+      uint32_t nq = 0, nh = 0, np = 0;  // parities of the next Q tile and halves of P, bit w: row tile w
+      int st = 0;                // ring stage of the next K or V tile
+      uint32_t par = 0;          // and its parity
+      bool ok = true;
+      auto take = [&](uint64_t* bar, uint32_t& parities, int w) {
+        ok = __all_sync(0xffffffffu, ok && sm100::mbar_wait(bar + w, (parities >> w) & 1u, &abort_flag));
+        parities ^= 1u << w;
+        sm100::tc_fence_after();
+      };
+      auto stage = [&]() {  // wait for the next tile; its stage
+        ok = __all_sync(0xffffffffu, ok && sm100::mbar_wait(&bars.full[st], par, &abort_flag));
+        sm100::tc_fence_after();
+        const int s = st;
+        if (++st == C::kStages) {
+          st = 0;
+          par ^= 1u;
         }
-        // no product is in flight when the columns are freed
-        sm100::mma_commit(&bars.last);
-        if (!sm100::mbar_wait_bounded(&bars.last, 0, 20000000ull) || !ok) atomicOr(&g_attn_err, kErrTimeout);
+        return s;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) sm100::mma_commit(bar);
+      };
+      auto qk = [&](int w, int s) {
+        const uint32_t a = q_lo + (uint32_t)w * (C::kQBytes >> 4), b = k_lo + (uint32_t)s * (C::kTileBytes >> 4);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k)
+            if (k < ks)
+              sm100::mma_ss(tmem + w * KT, a + (((k >> 2) * (kRows * 128) + (k & 3) * 32) >> 4), sm100::kSw128Hi,
+                            b + (((k >> 2) * (KT * 128) + (k & 3) * 32) >> 4), sm100::kSw128Hi, idesc_qk, k > 0);
+          sm100::mma_commit(&bars.s_full[w]);
+        }
+        __syncwarp();
+      };
+      auto pv_half = [&](int w, int s, bool first, int k0) {
+        const uint32_t b = v_lo + (uint32_t)s * (C::kTileBytes >> 4) + k0 * (2048 >> 4);
+        if (leader) {
+#pragma unroll
+          for (int k = 0; k < KT / 32; ++k)
+            sm100::mma_ts(tmem + C::kTiles * KT + w * DP, tmem + w * KT + (k0 + k) * 8, b + k * (2048 >> 4),
+                          sm100::kSw128Hi, idesc_pv, !first || k0 + k > 0);
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int w, int s, bool first) {
+        take(bars.p_half, nh, w);
+        if (ok) pv_half(w, s, first, 0);
+        take(bars.p_ready, np, w);
+        if (ok) pv_half(w, s, first, KT / 32);
+      };
+      for (int pi = 0; ok; ++pi) {
+        const ChunkPiece* c = piece(pi);
+        ok = __all_sync(0xffffffffu, c != nullptr);
+        if (!ok || !c->valid) break;
+        const bool keys = c->o.hi > c->o.lo;
+        const int act = c->o.rows > kRows ? 2 : 1;
+        const int cnt = c->o.j1 - c->o.j0;
+        __syncwarp();
+        if (leader) piece_done(pi);
+        if (!keys) continue;
+        int kst = stage();
+        for (int w = 0; w < act; ++w) {
+          take(bars.q_ready, nq, w);
+          if (ok) qk(w, kst);
+        }
+        if (ok) commit(&bars.empty[kst]);
+        for (int i = 0; ok && i < cnt; ++i) {
+          const bool more = i + 1 < cnt;
+          const int vst = stage();
+          pv(0, vst, i == 0);
+          if (!ok) break;
+          if (more) {
+            kst = stage();
+            if (ok) qk(0, kst);
+          } else {
+            commit(&bars.o_full[0]);
+          }
+          if (act == 2) {
+            pv(1, vst, i == 0);
+            if (!ok) break;
+            if (more) qk(1, kst);
+            else commit(&bars.o_full[1]);
+          }
+          commit(&bars.empty[vst]);
+          if (more) commit(&bars.empty[kst]);
+        }
       }
+      // no product is in flight when the columns are freed
+      commit(&bars.last);
+      if ((!sm100::mbar_wait_bounded(&bars.last, 0, 20000000ull) || !ok) && leader) atomicOr(&g_attn_err, kErrTimeout);
     }
   } else if (warp < 4 * C::kTiles) {  // ---- softmax: one row per thread ----
     sm100::regs_inc<kSoftmaxRegs>();
@@ -269,21 +334,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool begun = false, ok = true;
     // Q rows of a piece, the warp's 32: loaded to registers while the piece before
     // it ends, then stored K-major with the 128-byte swizzle (zeros behind the rows)
-    constexpr int kCols = DP / 8;  // 16-byte chunks per row
-    uint4 qreg[kCols];
+    // (an access of the warp is 4 rows x 128 bytes: row 4 j + lane / 8, 64-channel block b)
+    constexpr int kCols = DP / 8, kBlk = DP / 64;  // 16-byte chunks and blocks per row
+    uint4 qreg[8 * kBlk];
+    const int lrow = lane >> 3, lch = lane & 7;
     const int wrow = w * kRows + (warp & 3) * 32;  // first row of the warp within an item
     auto active = [&](const ChunkPiece* c) { return c->valid && c->o.hi > c->o.lo && c->o.rows > w * kRows; };
     auto load_q = [&](const ChunkPiece* c) {
-      const uint16_t* base = p.q + (int64_t)(c->o.s.t0 + c->tok0) * p.q_stride + (int64_t)c->o.h * p.G * p.D;
+      const uint16_t* base = p.q + (int64_t)(c->o.s.t0 + c->tok0) * p.q_stride + (int64_t)c->o.h * p.G * p.D + lch * 8;
       const int rows = active(c) ? c->o.rows : 0, rem0 = c->rem0;
 #pragma unroll
-      for (int i = 0; i < kCols; ++i) {
-        const int e = i * 32 + lane, qr = wrow + e / kCols, ch = e % kCols;
-        const int tok = attn_div_g(p, rem0 + qr), head = rem0 + qr - tok * p.G;
-        qreg[i] = make_uint4(0, 0, 0, 0);
-        if (qr < rows && ch * 8 < p.D)
-          qreg[i] = __ldg(reinterpret_cast<const uint4*>(base + (int64_t)tok * p.q_stride + head * p.D + ch * 8));
+      for (int j = 0; j < 8; ++j) {
+        const int x = wrow + 4 * j + lrow;
+        const int tok = p.div_g.div(rem0 + x), head = rem0 + x - tok * p.G;
+        const uint16_t* src = base + (int64_t)tok * p.q_stride + head * p.D;
+#pragma unroll
+        for (int b = 0; b < kBlk; ++b) {
+          qreg[j * kBlk + b] = make_uint4(0, 0, 0, 0);
+          if (x < rows && b * 64 + lch * 8 < p.D) qreg[j * kBlk + b] = __ldg(reinterpret_cast<const uint4*>(src + b * 64));
+        }
       }
+    };
+    // the lane's chunk of row 4 j + lrow of the warp's 32, block b, in the Q tile
+    unsigned char* qlane = qw + ((warp & 3) * 32 + lrow) * 128;
+    auto q_at = [&](int j, int b) {  // (4 j + lrow) & 7 = lrow + 4 (j & 1)
+      return reinterpret_cast<uint4*>(qlane + j * 512 + b * (kRows * 128) + ((lch ^ (lrow + 4 * (j & 1))) << 4));
     };
     const ChunkPiece* c = piece(0);
     ok = __all_sync(0xffffffffu, c != nullptr);
@@ -295,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         attn_write_desc(p, blockIdx.x, c->last_cta, &c->o);
         begun = true;
       }
-      const int tok = attn_div_g(p, c->rem0 + row);
+      const int tok = p.div_g.div(c->rem0 + row);
       const int64_t orow =
           (int64_t)(c->o.s.t0 + c->tok0 + tok) * p.Hq + c->o.h * p.G + c->rem0 + row - tok * p.G;  // of out and lse
       if (c->o.hi <= c->o.lo && mine) {
@@ -309,14 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ref = neg_inf(), l = 0.f;  // reference (log2 units) and sum of the row's weights
       if (act) {
 #pragma unroll
-        for (int i = 0; i < kCols; ++i) {
-          const int e = i * 32 + lane, qr = (warp & 3) * 32 + e / kCols, ch = e % kCols;
-          *reinterpret_cast<uint4*>(qw + (ch >> 3) * (kRows * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = qreg[i];
-        }
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int b = 0; b < kBlk; ++b) *q_at(j, b) = qreg[j * kBlk + b];
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&bars.q_ready[w]);
-        int lo = 0, hi = 0;
+        int lo = 0, hi = INT32_MAX;  // of a row that is not there: nothing to mask
         if (mine) {
           hi = attn_keys(p, c->o.s.start + c->tok0 + tok + 1);
           lo = p.window ? max(0, hi - p.window) : 0;
@@ -346,17 +420,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int b = 0; b < KT / 32; ++b) sm100::tmem_ld_wait(x[b]);
             const int clo = lo - key0, chi = hi - key0;  // the row's visible columns
-            if (__any_sync(0xffffffffu, clo > 0 || chi < KT)) {
+            const bool edge = __any_sync(0xffffffffu, clo > 0 || chi < KT);
+            if (edge) {
 #pragma unroll
               for (int e = 0; e < KT; ++e)
                 if (e < clo || e >= chi) x[e / 32][e % 32] = 0xff800000u;
             }
-            float mx = neg_inf();
+            float mx4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
             for (int e = 0; e < KT; e += 2)
-              mx = max3(mx, __uint_as_float(x[e / 32][e % 32]), __uint_as_float(x[e / 32][e % 32 + 1]));
-            mx *= p.scale_log2;
-            const bool grow = mx > ref + kLazy;  // also the first visible key's tile
+              mx4[e / 2 % 4] =
+                  max3(mx4[e / 2 % 4], __uint_as_float(x[e / 32][e % 32]), __uint_as_float(x[e / 32][e % 32 + 1]));
+            const float mx = p.scale_log2 * max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]);
+            const bool grow = mx > ref + kLazy;  // also the first visible key's tile; not a NaN
             if (__any_sync(0xffffffffu, grow)) {
               const float nref = grow ? mx : ref;
               const float corr = grow ? ex2(ref - nref) : 1.f;
@@ -375,22 +451,55 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             const float base = ref == neg_inf() ? 0.f : -ref;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int b = 0; b < KT / 32; ++b) {
+            const uint64_t scale2 = sm100::f2_pack(p.scale_log2, p.scale_log2), base2 = sm100::f2_pack(base, base);
+            // no masked key, infinity or NaN in any row of the warp: some weights by
+            // polynomial, so that the special function unit (16 results a clock and SM:
+            // 2048 clocks for a pair of tiles, as long as their products) is not what bounds
+            const bool plain = __all_sync(0xffffffffu, !edge && mx < 1e38f);
+            uint64_t sum2[2] = {0, 0};
+            auto weights = [&](auto poly, int b) {
               uint32_t pk[16];
 #pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float u = ex2(fmaf(__uint_as_float(x[b][e]), p.scale_log2, base));
-                const float v = ex2(fmaf(__uint_as_float(x[b][e + 1]), p.scale_log2, base));
-                sum[e % 4] += u;
-                sum[e % 4 + 1] += v;
-                pk[e / 2] = pack2<BF16>(u, v);
+              for (int e = 0; e < 16; ++e) {
+                const uint64_t y = sm100::f2_fma(
+                    sm100::f2_pack(__uint_as_float(x[b][2 * e]), __uint_as_float(x[b][2 * e + 1])), scale2, base2);
+                uint64_t v;
+                float u0, u1;
+                if (decltype(poly)::value && e * kPolyPairs / 16 != (e + 1) * kPolyPairs / 16) {
+                  v = exp2_pair(y);
+                  sm100::f2_unpack(v, u0, u1);
+                } else {
+                  sm100::f2_unpack(y, u0, u1);
+                  u0 = ex2(u0);
+                  u1 = ex2(u1);
+                  v = sm100::f2_pack(u0, u1);
+                }
+                sum2[e & 1] = sm100::f2_add(sum2[e & 1], v);
+                pk[e] = pack2<BF16>(u0, u1);
               }
               sm100::tmem_st16(s_t + b * 16, pk);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            };
+            auto all = [&](auto poly) {
+#pragma unroll
+              for (int b = 0; b < KT / 32; ++b) {
+                weights(poly, b);
+                if (b == KT / 64 - 1) {  // the first half's product may start
+                  sm100::tmem_st_wait();
+                  sm100::tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) sm100::mbar_arrive(&bars.p_half[w]);
+                }
+              }
+            };
+            if (plain) all(std::true_type{});
+            else all(std::false_type{});
+            float s0, s1, s2, s3;
+            sm100::f2_unpack(sum2[0], s0, s1);
+            sm100::f2_unpack(sum2[1], s2, s3);
+            l += (s0 + s1) + (s2 + s3);
             sm100::tmem_st_wait();
+          } else if (lane == 0) {
+            sm100::mbar_arrive(&bars.p_half[w]);
           }
           sm100::tc_fence_before();
           __syncwarp();
@@ -442,16 +551,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (whole) {
             __syncwarp();
             const int rows = c->o.rows, rem0 = c->rem0;
-            uint16_t* base = p.out + ((int64_t)(c->o.s.t0 + c->tok0) * p.Hq + (int64_t)c->o.h * p.G) * p.D;
+            uint16_t* base =
+                p.out + ((int64_t)(c->o.s.t0 + c->tok0) * p.Hq + (int64_t)c->o.h * p.G) * p.D + lch * 8;
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) {
-              const int e = i * 32 + lane, qr = (warp & 3) * 32 + e / kCols, ch = e % kCols;
-              const int ir = w * kRows + qr;
-              const int t = attn_div_g(p, rem0 + ir), head = rem0 + ir - t * p.G;
-              const uint4 v =
-                  *reinterpret_cast<const uint4*>(qw + (ch >> 3) * (kRows * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4));
-              if (ir < rows && ch * 8 < p.D)
-                *reinterpret_cast<uint4*>(base + ((int64_t)t * p.Hq + head) * p.D + ch * 8) = v;
+            for (int j = 0; j < 8; ++j) {
+              const int x = wrow + 4 * j + lrow;
+              const int t = p.div_g.div(rem0 + x), head = rem0 + x - t * p.G;
+              uint16_t* dst = base + ((int64_t)t * p.Hq + head) * p.D;
+#pragma unroll
+              for (int b = 0; b < kBlk; ++b) {
+                const uint4 v = *q_at(j, b);
+                if (x < rows && b * 64 + lch * 8 < p.D) *reinterpret_cast<uint4*>(dst + b * 64) = v;
+              }
             }
           }
           if (mine) {

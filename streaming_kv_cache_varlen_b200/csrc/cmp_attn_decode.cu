@@ -125,9 +125,9 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
         const bool need = has && key < o.hi && key + (1 << run_shift) > o.lo;
         int row = no_row;
         if (need) {
-          const int pg = key / p.page;
+          const int pg = p.div_page.div(key);
           const int e = pg < p.table_stride ? __ldg(trow + pg) : -1;
-          if (e >= 0 && e < p.block_num) row = e * p.page + key % p.page;
+          if (e >= 0 && e < p.block_num) row = e * p.page + (key - pg * p.page);
           else atomicOr(&g_attn_err, kErrIndex);
         }
         const unsigned m = __ballot_sync(0xffffffffu, need);
@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
       lo[i] = hi[i] = 0;
       if (ok) attn_row_range(p, o.s, o.row0 + r, lo[i], hi[i]);
       const int rr = o.row0 + r;
-      const uint16_t* src = p.q + (int64_t)(o.s.t0 + rr / p.G) * p.q_stride + (int64_t)(o.h * p.G + rr % p.G) * p.D;
+      const int tok = p.div_g.div(rr);
+      const uint16_t* src = p.q + (int64_t)(o.s.t0 + tok) * p.q_stride + (int64_t)(o.h * p.G + rr - tok * p.G) * p.D;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int c = k * 16 + 2 * t4;
