@@ -18,8 +18,6 @@
 // common factor cancels in out and lse.
 #include "cmp_attn.cuh"
 
-#include <type_traits>
-
 namespace cmp {
 namespace {
 
@@ -29,7 +27,6 @@ constexpr int kThreads = 12 * 32;
 // (128 values), the other 4 give theirs up. 8 * 216 + 4 * 72 = 12 * 168, the launch's.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 constexpr int kPieces = 4;                // pieces the scheduler runs ahead
-constexpr int kPolyPairs = 6;             // of 16 pairs of weights, those that exp2_pair takes
 constexpr float kLazy = 8.f;              // log2 of the largest weight
 
 __device__ unsigned g_attn_err;
@@ -61,34 +58,6 @@ struct ChunkPiece {
   bool valid;      // false: the CTA's part ends here
 };
 
-// 2^x of two values below 2^7 without the special function unit: x = n + f with n
-// the nearest integer (adding 1.5 * 2^23 leaves n in the low bits of the sum), a
-// polynomial for 2^f on [-1/2, 1/2], n added to its exponent. The polynomial is the
-// degree-5 one of least maximal relative error, from a weighted least-squares fit
-// iterated on the error (Lawson); with its roundings it is off by at most 3.6 * 2^-24,
-// as ex2.approx (2^-22). Values below -127.5 give 0; not for NaN or infinities.
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t v) {
-  constexpr float kMagic = 12582912.f;
-  float a, b;
-  sm100::f2_unpack(v, a, b);
-  const uint64_t x = sm100::f2_pack(fmaxf(a, -128.f), fmaxf(b, -128.f));
-  const uint64_t t = sm100::f2_add(x, sm100::f2_pack(kMagic, kMagic));
-  const uint64_t n = sm100::f2_add(t, sm100::f2_pack(-kMagic, -kMagic));
-  const uint64_t f = sm100::f2_fma(n, sm100::f2_pack(-1.f, -1.f), x);
-  auto c = [](float k) { return sm100::f2_pack(k, k); };
-  uint64_t p = sm100::f2_fma(c(0x1.5c08e4p-10f), f, c(0x1.3d0c52p-7f));
-  p = sm100::f2_fma(p, f, c(0x1.c6b6e4p-5f));
-  p = sm100::f2_fma(p, f, c(0x1.ebf918p-3f));
-  p = sm100::f2_fma(p, f, c(0x1.62e428p-1f));
-  p = sm100::f2_fma(p, f, c(0x1.000002p+0f));
-  float pa, pb, ta, tb;
-  sm100::f2_unpack(p, pa, pb);
-  sm100::f2_unpack(t, ta, tb);
-  const int ra = max(__float_as_int(pa) + (int)(__float_as_uint(ta) << 23), 0);
-  const int rb = max(__float_as_int(pb) + (int)(__float_as_uint(tb) << 23), 0);
-  return sm100::f2_pack(__int_as_float(ra), __int_as_float(rb));
-}
-
 // The largest of three; NaN if one of them is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
@@ -111,7 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int64_t warp_sum[kThreads / 32];
   __shared__ int abort_flag;
   __shared__ uint32_t tmem_slot;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = sm100::uniform(tid >> 5), lane = tid & 31;
 
   pdl_trigger();
   if (tid == 0) {
@@ -127,11 +96,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       sm100::mbar_init(&bars.p_ready[w], 4);
       sm100::mbar_init(&bars.o_full[w], 1);
     }
+    sm100::mbar_init(&bars.last, 1);
     for (int i = 0; i < kPieces; ++i) {
       sm100::mbar_init(&bars.piece_full[i], 1);
       sm100::mbar_init(&bars.piece_empty[i], 4 * C::kTiles + 2);  // softmax warps, products, producer
     }
-    sm100::mbar_init(&bars.last, 1);
     sm100::fence_barrier_init();
   }
   if (warp == 8) sm100::tmem_alloc(&tmem_slot, 512);
@@ -340,12 +309,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lrow = lane >> 3, lch = lane & 7;
     const int wrow = w * kRows + (warp & 3) * 32;  // first row of the warp within an item
     auto active = [&](const ChunkPiece* c) { return c->valid && c->o.hi > c->o.lo && c->o.rows > w * kRows; };
-    auto load_q = [&](const ChunkPiece* c) {
+    // lrow as a value the compiler knows nothing of: what follows from it is computed
+    // where it is used, not kept in registers across the tiles
+    auto fresh = [&]() {
+      int v = lrow;
+      asm volatile("" : "+r"(v));
+      return v;
+    };
+    auto load_q = [&](const ChunkPiece* c, bool there) {  // not there: zeros (and no register stays live)
       const uint16_t* base = p.q + (int64_t)(c->o.s.t0 + c->tok0) * p.q_stride + (int64_t)c->o.h * p.G * p.D + lch * 8;
-      const int rows = active(c) ? c->o.rows : 0, rem0 = c->rem0;
+      const int rows = there && active(c) ? c->o.rows : 0, rem0 = c->rem0, row = fresh();
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int x = wrow + 4 * j + lrow;
+        const int x = wrow + 4 * j + row;
         const int tok = p.div_g.div(rem0 + x), head = rem0 + x - tok * p.G;
         const uint16_t* src = base + (int64_t)tok * p.q_stride + head * p.D;
 #pragma unroll
@@ -356,13 +332,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     // the lane's chunk of row 4 j + lrow of the warp's 32, block b, in the Q tile
-    unsigned char* qlane = qw + ((warp & 3) * 32 + lrow) * 128;
-    auto q_at = [&](int j, int b) {  // (4 j + lrow) & 7 = lrow + 4 (j & 1)
-      return reinterpret_cast<uint4*>(qlane + j * 512 + b * (kRows * 128) + ((lch ^ (lrow + 4 * (j & 1))) << 4));
+    auto q_at = [&](int row, int j, int b) {  // row = lrow; (4 j + lrow) & 7 = lrow + 4 (j & 1)
+      return reinterpret_cast<uint4*>(qw + ((warp & 3) * 32 + row) * 128 + j * 512 + b * (kRows * 128) +
+                                      ((lch ^ (row + 4 * (j & 1))) << 4));
     };
-    const ChunkPiece* c = piece(0);
-    ok = __all_sync(0xffffffffu, c != nullptr);
-    if (ok) load_q(c);
+    const ChunkPiece* c = &pieces[0];
+    ok = __all_sync(0xffffffffu, piece(0) != nullptr);
+    load_q(c, ok);
     for (int pi = 0; ok && c->valid; ++pi) {
       const int row = w * kRows + r;  // of the item
       const bool mine = row < c->o.rows;
@@ -370,10 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         attn_write_desc(p, blockIdx.x, c->last_cta, &c->o);
         begun = true;
       }
-      const int tok = p.div_g.div(c->rem0 + row);
-      const int64_t orow =
-          (int64_t)(c->o.s.t0 + c->tok0 + tok) * p.Hq + c->o.h * p.G + c->rem0 + row - tok * p.G;  // of out and lse
+      auto out_row = [&]() {  // of out and lse
+        const int tok = p.div_g.div(c->rem0 + row);
+        return (int64_t)(c->o.s.t0 + c->tok0 + tok) * p.Hq + c->o.h * p.G + c->rem0 + row - tok * p.G;
+      };
       if (c->o.hi <= c->o.lo && mine) {
+        const int64_t orow = out_row();
         for (int e = 0; e < p.D; e += 8)
           *reinterpret_cast<uint4*>(p.out + orow * p.D + e) = make_uint4(0, 0, 0, 0);
         if (p.lse) p.lse[orow] = neg_inf();
@@ -383,16 +361,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool warp_rows = wrow < c->o.rows;
       float ref = neg_inf(), l = 0.f;  // reference (log2 units) and sum of the row's weights
       if (act) {
+        const int qrow = fresh();
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-          for (int b = 0; b < kBlk; ++b) *q_at(j, b) = qreg[j * kBlk + b];
+          for (int b = 0; b < kBlk; ++b) *q_at(qrow, j, b) = qreg[j * kBlk + b];
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(&bars.q_ready[w]);
         int lo = 0, hi = INT32_MAX;  // of a row that is not there: nothing to mask
         if (mine) {
-          hi = attn_keys(p, c->o.s.start + c->tok0 + tok + 1);
+          hi = attn_keys(p, c->o.s.start + c->tok0 + p.div_g.div(c->rem0 + row) + 1);
           lo = p.window ? max(0, hi - p.window) : 0;
         }
         for (int i = 0; i < cnt; ++i, n += 2) {
@@ -412,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           ok = sm100::mbar_wait(&bars.s_full[w], ns++ & 1u, &abort_flag) && ok;
           ok = __all_sync(0xffffffffu, ok);
-            sm100::tc_fence_after();
+          if (!ok) break;
+          sm100::tc_fence_after();
           if (warp_rows) {
             uint32_t x[KT / 32][32];
 #pragma unroll
@@ -452,47 +432,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const float base = ref == neg_inf() ? 0.f : -ref;
             const uint64_t scale2 = sm100::f2_pack(p.scale_log2, p.scale_log2), base2 = sm100::f2_pack(base, base);
-            // no masked key, infinity or NaN in any row of the warp: some weights by
-            // polynomial, so that the special function unit (16 results a clock and SM:
-            // 2048 clocks for a pair of tiles, as long as their products) is not what bounds
-            const bool plain = __all_sync(0xffffffffu, !edge && mx < 1e38f);
             uint64_t sum2[2] = {0, 0};
-            auto weights = [&](auto poly, int b) {
+#pragma unroll
+            for (int b = 0; b < KT / 32; ++b) {
               uint32_t pk[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const uint64_t y = sm100::f2_fma(
-                    sm100::f2_pack(__uint_as_float(x[b][2 * e]), __uint_as_float(x[b][2 * e + 1])), scale2, base2);
-                uint64_t v;
                 float u0, u1;
-                if (decltype(poly)::value && e * kPolyPairs / 16 != (e + 1) * kPolyPairs / 16) {
-                  v = exp2_pair(y);
-                  sm100::f2_unpack(v, u0, u1);
-                } else {
-                  sm100::f2_unpack(y, u0, u1);
-                  u0 = ex2(u0);
-                  u1 = ex2(u1);
-                  v = sm100::f2_pack(u0, u1);
-                }
-                sum2[e & 1] = sm100::f2_add(sum2[e & 1], v);
+                sm100::f2_unpack(sm100::f2_fma(sm100::f2_pack(__uint_as_float(x[b][2 * e]), __uint_as_float(x[b][2 * e + 1])),
+                                               scale2, base2),
+                                 u0, u1);
+                u0 = ex2(u0);
+                u1 = ex2(u1);
+                sum2[e & 1] = sm100::f2_add(sum2[e & 1], sm100::f2_pack(u0, u1));
                 pk[e] = pack2<BF16>(u0, u1);
               }
               sm100::tmem_st16(s_t + b * 16, pk);
-            };
-            auto all = [&](auto poly) {
-#pragma unroll
-              for (int b = 0; b < KT / 32; ++b) {
-                weights(poly, b);
-                if (b == KT / 64 - 1) {  // the first half's product may start
-                  sm100::tmem_st_wait();
-                  sm100::tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) sm100::mbar_arrive(&bars.p_half[w]);
-                }
+              if (b == KT / 64 - 1) {  // the first half's product may start
+                sm100::tmem_st_wait();
+                sm100::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) sm100::mbar_arrive(&bars.p_half[w]);
               }
-            };
-            if (plain) all(std::true_type{});
-            else all(std::false_type{});
+            }
             float s0, s1, s2, s3;
             sm100::f2_unpack(sum2[0], s0, s1);
             sm100::f2_unpack(sum2[1], s2, s3);
@@ -510,10 +472,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---- end of the piece; the next one's Q is loaded meanwhile ----
-      const ChunkPiece* next = piece(pi + 1);
-      ok = __all_sync(0xffffffffu, next != nullptr);
+      const ChunkPiece* next = &pieces[(pi + 1) % kPieces];
+      ok = __all_sync(0xffffffffu, piece(pi + 1) != nullptr);
+      load_q(next, ok);
       if (!ok) break;
-      load_q(next);
       if (act) {
         ok = sm100::mbar_wait(&bars.o_full[w], no++ & 1u, &abort_flag);
         ok = __all_sync(0xffffffffu, ok);
@@ -550,24 +512,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (whole) {
             __syncwarp();
-            const int rows = c->o.rows, rem0 = c->rem0;
+            const int rows = c->o.rows, rem0 = c->rem0, qrow = fresh();
             uint16_t* base =
                 p.out + ((int64_t)(c->o.s.t0 + c->tok0) * p.Hq + (int64_t)c->o.h * p.G) * p.D + lch * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const int x = wrow + 4 * j + lrow;
+              const int x = wrow + 4 * j + qrow;
               const int t = p.div_g.div(rem0 + x), head = rem0 + x - t * p.G;
               uint16_t* dst = base + ((int64_t)t * p.Hq + head) * p.D;
 #pragma unroll
               for (int b = 0; b < kBlk; ++b) {
-                const uint4 v = *q_at(j, b);
+                const uint4 v = *q_at(qrow, j, b);
                 if (x < rows && b * 64 + lch * 8 < p.D) *reinterpret_cast<uint4*>(dst + b * 64) = v;
               }
             }
           }
           if (mine) {
             if (!whole) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(ref, l);
-            else if (p.lse) p.lse[orow] = attn_lse(ref, l);
+            else if (p.lse) p.lse[out_row()] = attn_lse(ref, l);
           }
         }
         sm100::tc_fence_before();

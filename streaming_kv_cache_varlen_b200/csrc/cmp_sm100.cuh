@@ -197,6 +197,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_
       : "memory");
 }
 
+// Whole warp: lane 0's value, which the compiler then knows to be the same in all
+// lanes (it may live in a uniform register, where the operands of tcgen05.mma must be).
+template <class T>
+__device__ __forceinline__ T uniform(T v) {
+  return (T)__shfl_sync(0xffffffffu, v, 0);
+}
+
 // Whole warp: true in one lane, the same one every time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
