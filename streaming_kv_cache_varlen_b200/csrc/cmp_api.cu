@@ -305,13 +305,12 @@ struct AttnPath {
 
 AttnPath attn_path(const cmp_attn_dims& d) {
   AttnPath a{};
-  cmp::AttnParams p{};
-  p.D = (int)d.D;
   const int64_t len = d.max_len && d.max_len < d.T ? d.max_len : d.T;
-  a.chunk = len * (d.Hq / d.Hk) > cmp::kAttnDecodeRows;
-  a.m = a.chunk ? cmp::attn_chunk_rows(p.D) : cmp::kAttnDecodeRows;
-  a.ctas = a.chunk ? sm_count_cached() : cmp::attn_decode_ctas(p, sm_count_cached());
-  a.key_tile = a.chunk ? cmp::attn_chunk_key_tile(p.D) : 64;
+  const int64_t rows = len * (d.Hq / d.Hk);
+  a.chunk = rows > cmp::kAttnDecodeRows;
+  a.m = a.chunk ? cmp::attn_chunk_rows((int)d.D) : cmp::attn_decode_rows(rows);
+  a.ctas = a.chunk ? sm_count_cached() : cmp::attn_decode_ctas((int)d.D, sm_count_cached());
+  a.key_tile = a.chunk ? cmp::attn_chunk_key_tile((int)d.D) : 64;
   const size_t slots = (size_t)a.ctas * 2 * a.m;
   a.part = 0;
   a.ml = a.part + slots * cmp::attn_padded((int)d.D) * sizeof(float);
@@ -743,7 +742,7 @@ int cmp_paged_attention(const void* q, const void* k_cache, const void* v_cache,
   note_word_device();
   const cudaError_t e =
       a.chunk ? launch(CMP_KERNEL_ATTN_CHUNK, s, [&] { return cmp::launch_attn_chunk(p, kmap, vmap, s, a.ctas); })
-              : launch(CMP_KERNEL_ATTN_DECODE, s, [&] { return cmp::launch_attn_decode(p, kmap, vmap, s, a.ctas); });
+              : launch(CMP_KERNEL_ATTN_DECODE, s, [&] { return cmp::launch_attn_decode(p, kmap, vmap, s, a.ctas, a.m); });
   if (e != cudaSuccess) return CMP_ERR_CUDA;
   if (launch(CMP_KERNEL_ATTN_COMBINE, s, [&] { return cmp::launch_attn_combine(p, a.m, a.ctas, s); }) != cudaSuccess)
     return CMP_ERR_CUDA;

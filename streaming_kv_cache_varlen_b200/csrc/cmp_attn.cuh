@@ -356,10 +356,13 @@ inline int attn_padded(int D) { return (D + 63) / 64 * 64; }
 // one head over 1 << run_shift rows, landing 128-byte swizzled.
 bool attn_cache_map(CUtensorMap* m, const void* cache, const AttnParams& p);
 
+// Decoding: items of 8 or 16 rows (`m`).
+constexpr int kAttnDecodeRows = 16;  // the most rows per key head and sequence it runs with
+int attn_decode_rows(int64_t rows);
+int attn_decode_ctas(int D, int sms);
 cudaError_t launch_attn_decode(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s,
-                               int ctas);
-int attn_decode_ctas(const AttnParams& p, int sms);
-constexpr int kAttnDecodeRows = 16;  // rows per item of the decode kernel
+                               int ctas, int m);
+cudaError_t attn_decode_take_error(unsigned* word);
 // Chunks: 128-row MMA tiles, one CTA per SM.
 int attn_chunk_rows(int D);      // rows per item
 int attn_chunk_key_tile(int D);  // keys per tile
@@ -367,6 +370,5 @@ cudaError_t launch_attn_chunk(const AttnParams& p, const CUtensorMap& k, const C
                               int ctas);
 cudaError_t attn_chunk_take_error(unsigned* word);
 cudaError_t launch_attn_combine(const AttnParams& p, int m, int ctas, cudaStream_t s);
-cudaError_t attn_decode_take_error(unsigned* word);
 
 }  // namespace cmp

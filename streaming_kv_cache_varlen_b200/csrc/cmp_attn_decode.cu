@@ -5,32 +5,42 @@
 // One producer warp streams tiles of 64 keys and their values through a ring of
 // shared-memory stages by TMA (each lane issues one box: 64 channels over a run
 // of rows inside one page, and looks up that run's page). Four consumer warps take
-// 16 keys of every tile each: S = Q K^T on 16 x 16 x D with mma.sync, an online
-// softmax in registers (running maximum and sum per warp, so the warps never wait
-// for one another inside an item), and O += P V from the same registers. The
-// rows of a tile are few (16 at most), so the tensor work is a few percent of the
-// stream's time at any rate; what counts is that the stream never pauses. At the
-// end of an item the four warps' accumulators are added in shared memory.
+// 16 keys of a tile each.
+// The products are transposed, so that the keys fill the 16 rows of mma.sync and
+// the few queries its 8 columns (8 rows per item; 16 are two column blocks):
+//   S^T = K Q^T,  O^T += V^T P^T
+// (with the queries as rows, an item of 8 rows or fewer spent twice the products
+// and registers: 635 us at 128 batches of 24 heads of 192, as a warp has little
+// else to overlap them with). Softmax in registers, statistics per warp, so the
+// warps never wait for one another inside an item; a row's reference is moved (and
+// the accumulator rescaled) only when a score exceeds it by more than kLazy, so
+// that a step needs no shuffle. At the end of an item the warps' accumulators are
+// added in shared memory, in a fixed order.
 #include "cmp_attn.cuh"
 
 namespace cmp {
 namespace {
 
-constexpr int kM = kAttnDecodeRows;
-constexpr int kKT = 64;                      // keys per tile
-constexpr int kWarps = 4;                    // consumer warps; warp kWarps produces
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kKT = 64;                       // keys per tile
+constexpr float kLazy = 8.f;                  // log2 of the largest weight
 
 __device__ unsigned g_attn_err;
 
-template <int DP>
+// DP: padded channels; NB: blocks of 8 rows per item
+template <int DP, int NB>
 struct DecodeCfg {
-  static constexpr int kTileBytes = kKT * DP * 2;        // K or V
+  static constexpr int kM = 8 * NB;
+  static constexpr int kTileBytes = kKT * DP * 2;  // K or V
   static constexpr int kStageBytes = 2 * kTileBytes;
+  // Eight consumer warps per SM where their registers allow: two CTAs of four, or
+  // one of eight whose halves (groups) take every other tile.
   static constexpr int kCtasPerSm = DP <= 128 ? 2 : 1;
-  static constexpr int kStages = DP <= 64 ? 6 : DP <= 128 ? 3 : DP <= 192 ? 4 : 3;
-  static constexpr int kPitch = DP + 8;                   // floats per row of the merge buffer
-  static constexpr int kMergeBytes = kM * kPitch * 4;
+  static constexpr int kGroups = DP > 128 && NB == 1 ? 2 : 1;
+  static constexpr int kWarps = 4 * kGroups;  // consumers; warp kWarps produces
+  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kStages = (kCtasPerSm == 2 ? 98304 : 196608) / kStageBytes;
+  static constexpr int kPitch = DP + 4;            // floats per row of a merge buffer
+  static constexpr int kMergeBytes = kGroups * kM * kPitch * 4;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kMergeBytes;
 };
 
@@ -45,6 +55,12 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a)
                : "memory");
+}
+// An 8 x 8 matrix of 16-bit elements (two of a row per thread), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 template <bool BF16>
@@ -61,21 +77,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+template <int kWarps>
 __device__ __forceinline__ void bar_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); }
 
-// Byte offset of (key, 16-byte chunk) in a tile that TMA wrote with the 128-byte
-// swizzle: blocks of 64 channels, one 128-byte row per key.
-__device__ __forceinline__ uint32_t tile_at(int key, int chunk) {
-  return (uint32_t)((chunk >> 3) * (kKT * 128) + key * 128 + (((chunk & 7) ^ (key & 7)) << 4));
-}
-
-template <bool BF16, int DP>
-__global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
+template <bool BF16, int DP, int NB>
+__global__ void __launch_bounds__(DecodeCfg<DP, NB>::kThreads, DecodeCfg<DP, NB>::kCtasPerSm)
     attn_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const AttnParams p) {
-  using C = DecodeCfg<DP>;
-  constexpr int KS = DP / 16;  // K steps of Q K^T
-  constexpr int NT = DP / 8;   // 8-column blocks of the accumulator
+  using C = DecodeCfg<DP, NB>;
+  constexpr int KS = DP / 16;  // 16-channel steps
+  constexpr int kM = C::kM, kGroups = C::kGroups, kWarps = C::kWarps, kThreads = C::kThreads;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* ring = &sm100::smem_align1024<unsigned char>(smem_raw);
   float* merge = reinterpret_cast<float*>(ring + (size_t)C::kStages * C::kStageBytes);
@@ -91,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
     abort_flag = 0;
     for (int i = 0; i < C::kStages; ++i) {
       sm100::mbar_init(&full[i], 1);
-      sm100::mbar_init(&empty[i], kWarps);
+      sm100::mbar_init(&empty[i], 4);  // the warps of the group that takes the tile
     }
     sm100::fence_barrier_init();
   }
@@ -113,14 +124,14 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
     const uint32_t dst_off = (uint32_t)(which * C::kTileBytes + blk * (kKT * 128) + (run << run_shift) * 128);
     const int no_row = (int)(p.block_num * p.page);  // past the cache: zeros land
     sm100::Armed armed;
-    int n = 0;
+    int st = 0, n = 0;
+    uint32_t par = 0;
     bool alive = true;
     AttnPiece o;
     while (alive && walk.next(o)) {
       if (o.hi <= o.lo) continue;
       const int32_t* trow = p.table + (int64_t)o.b * p.table_stride;
       for (int j = o.j0; j < o.j1; ++j, ++n) {
-        const int st = n % C::kStages;
         const int key = j * kKT + (run << run_shift);
         const bool need = has && key < o.hi && key + (1 << run_shift) > o.lo;
         int row = no_row;
@@ -131,14 +142,18 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
           else atomicOr(&g_attn_err, kErrIndex);
         }
         const unsigned m = __ballot_sync(0xffffffffu, need);
-        if (n >= C::kStages) alive = sm100::mbar_wait(&empty[st], (uint32_t)(n / C::kStages - 1) & 1u, &abort_flag);
+        if (n >= C::kStages) alive = sm100::mbar_wait(&empty[st], par ^ 1u, &abort_flag);
         alive = __all_sync(0xffffffffu, alive);
         if (!alive) break;
         if (lane == 0) sm100::mbar_arrive_expect_tx(&full[st], (uint32_t)__popc(m) * box_bytes);
-        armed.note(st, (uint32_t)(n / C::kStages) & 1u);
+        armed.note(st, par);
         __syncwarp();
         if (need)
           sm100::tma_load_3d(ring + (size_t)st * C::kStageBytes + dst_off, map, &full[st], blk * 64, o.h, row);
+        if (++st == C::kStages) {
+          st = 0;
+          par ^= 1u;
+        }
       }
     }
     if (!sm100::drain_armed(full, C::kStages, armed) || !alive)
@@ -147,164 +162,207 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
   }
 
   // ---- consumers ----
-  const int g = lane >> 2, t4 = lane & 3;  // row (and row + 8) and column pair of a fragment
-  int n = 0;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int group = warp >> 2, quarter = warp & 3;
+  // byte offsets in a 64-channel block of a tile (one 128-byte row per key, 16-byte
+  // chunks XORed with key % 8) that this lane gives to ldmatrix, per 16-channel step:
+  // K rows as they lie, V to be transposed
+  uint32_t koff[4], voff[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int kk = quarter * 16 + (lane & 15), vk = quarter * 16 + (lane & 7) + ((lane >> 4) << 3);
+    koff[k] = (uint32_t)(kk * 128 + (((2 * k + (lane >> 4)) ^ (lane & 7)) << 4));
+    voff[k] = (uint32_t)(vk * 128 + (((2 * k + ((lane >> 3) & 1)) ^ (lane & 7)) << 4));
+  }
+  int st = 0, n = 0;  // ring stage and number of the next tile
+  uint32_t par = 0;
   AttnPiece o;
   bool begun = false;
   if (start.units == 0 && tid == 0) attn_write_desc(p, blockIdx.x, 0, nullptr);
   while (walk.next(o)) {
-    // Q fragments: rows g and g + 8; rows past the item are zeros
-    uint32_t qf[KS][4];
-    int lo[2], hi[2];
+    // Q^T fragments (row 8 nb + g, channels 2 t4, + 1 and + 8, + 9 of a step), zeros
+    // past the item's rows; visible keys of rows 8 nb + 2 t4 and + 1
+    uint32_t qf[KS][NB][2];
+    int lo[NB][2], hi[NB][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i;
+    for (int b = 0; b < NB; ++b) {
+      const int r = 8 * b + g;
       const bool ok = r < o.rows;
-      lo[i] = hi[i] = 0;
-      if (ok) attn_row_range(p, o.s, o.row0 + r, lo[i], hi[i]);
-      const int rr = o.row0 + r;
+      const int rr = o.row0 + (ok ? r : 0);
       const int tok = p.div_g.div(rr);
       const uint16_t* src = p.q + (int64_t)(o.s.t0 + tok) * p.q_stride + (int64_t)(o.h * p.G + rr - tok * p.G) * p.D;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int c = k * 16 + 2 * t4;
         const bool in = ok && k * 16 < p.D;
-        qf[k][i] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + c)) : 0u;
-        qf[k][i + 2] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + c + 8)) : 0u;
+        qf[k][b][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + c)) : 0u;
+        qf[k][b][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + c + 8)) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        lo[b][i] = hi[b][i] = 0;
+        if (8 * b + 2 * t4 + i < o.rows) attn_row_range(p, o.s, o.row0 + 8 * b + 2 * t4 + i, lo[b][i], hi[b][i]);
       }
     }
-    float acc[NT][4];
+    int lo_all, hi_all;  // keys that every row of the item sees
+    {
+      int x;
+      attn_row_range(p, o.s, o.row0, x, hi_all);
+      attn_row_range(p, o.s, o.row0 + o.rows - 1, lo_all, x);
+    }
+    float acc[KS][NB][4];  // O^T: channels 16 s + g (+ 8), rows 8 nb + 2 t4 (+ 1)
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int s = 0; s < KS; ++s)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-    float mrow[2] = {neg_inf(), neg_inf()}, lrow[2] = {0.f, 0.f};
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[s][b][e] = 0.f;
+    float ref[NB][2], l[NB][2];  // of rows 8 nb + 2 t4 (+ 1); l: this thread's keys only
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      ref[b][0] = ref[b][1] = neg_inf();
+      l[b][0] = l[b][1] = 0.f;
+    }
 
     if (o.hi > o.lo) {
       for (int j = o.j0; j < o.j1; ++j, ++n) {
-        const int st = n % C::kStages;
-        const bool ok = sm100::mbar_wait(&full[st], (uint32_t)(n / C::kStages) & 1u, &abort_flag);
-        unsigned char* kt = ring + (size_t)st * C::kStageBytes;
-        unsigned char* vt = kt + C::kTileBytes;
-        const int key0 = j * kKT + warp * 16;  // this warp's keys
-        if (ok && key0 < o.hi && key0 + 16 > o.lo) {
-          if (key0 < o.lo || key0 + 16 > o.hi) {
-            // values behind the sequence's end (or before the window) may hold
-            // anything, a NaN times a weight of 0 included: make them zeros
-            for (int i = lane; i < 16 * (DP / 8); i += 32) {
-              const int k = i & 15;
-              if (key0 + k < o.lo || key0 + k >= o.hi)
-                *reinterpret_cast<uint4*>(vt + tile_at(warp * 16 + k, i >> 4)) = make_uint4(0, 0, 0, 0);
+        if ((n & (kGroups - 1)) == group) {
+          const bool ok = sm100::mbar_wait(&full[st], par, &abort_flag);
+          unsigned char* kt = ring + (size_t)st * C::kStageBytes;
+          unsigned char* vt = kt + C::kTileBytes;
+          const int key0 = j * kKT + quarter * 16;  // this warp's keys
+          if (ok && key0 < o.hi && key0 + 16 > o.lo) {
+            if (key0 < o.lo || key0 + 16 > o.hi) {
+              // values behind the sequence's end (or before the window) may hold
+              // anything, a NaN times a weight of 0 included: make them zeros
+              for (int i = lane; i < 16 * (DP / 8); i += 32) {
+                const int k = i & 15, ch = i >> 4;
+                if (key0 + k < o.lo || key0 + k >= o.hi)
+                  *reinterpret_cast<uint4*>(vt + (ch >> 3) * (kKT * 128) + (quarter * 16 + k) * 128 + ((ch & 7) << 4)) =
+                      make_uint4(0, 0, 0, 0);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the stage's next TMA write comes after
+              __syncwarp();
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the stage's next TMA write comes after
-            __syncwarp();
-          }
-          // S = Q K^T: 16 rows x 16 keys
-          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-          const uint32_t kb = sm100::smem_u32(kt);
-          const int krow = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+            // S^T = K Q^T in two chains
+            float sa[NB][4], sb[NB][4];
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            if (k * 16 < p.D) {
-              uint32_t b[4];
-              ldsm4(kb + tile_at(krow, k * 2 + ((lane >> 3) & 1)), b);
-              mma16816<BF16>(s0, qf[k], b[0], b[1]);
-              mma16816<BF16>(s1, qf[k], b[2], b[3]);
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sa[b][e] = sb[b][e] = 0.f;
+            const uint32_t ka = sm100::smem_u32(kt), va = sm100::smem_u32(vt);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              uint32_t a[4];
+              ldsm4(ka + (k >> 2) * (kKT * 128) + koff[k & 3], a);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16816<BF16>(k & 1 ? sb[b] : sa[b], a, qf[k][b][0], qf[k][b][1]);
+            }
+            // keys g (e < 2) and g + 8, row e & 1
+            float x[NB][4];
+            bool grow = false;
+            const bool edge = key0 < lo_all || key0 + 16 > hi_all;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                x[b][e] = (sa[b][e] + sb[b][e]) * p.scale_log2;
+                const int key = key0 + g + (e >> 1) * 8;
+                if (edge && (key < lo[b][e & 1] || key >= hi[b][e & 1])) x[b][e] = neg_inf();
+                grow |= x[b][e] > ref[b][e & 1] + kLazy;
+              }
+            if (__any_sync(0xffffffffu, grow)) {  // also a row's first visible key
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  float mx = fmaxf(x[b][i], x[b][i + 2]);
+#pragma unroll
+                  for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                  const float nref = mx > ref[b][i] + kLazy ? mx : ref[b][i];
+                  const float corr = nref == neg_inf() ? 1.f : ex2(ref[b][i] - nref);
+                  ref[b][i] = nref;
+                  l[b][i] *= corr;
+#pragma unroll
+                  for (int s = 0; s < KS; ++s) {
+                    acc[s][b][i] *= corr;
+                    acc[s][b][i + 2] *= corr;
+                  }
+                }
+            }
+            uint32_t pf[NB][2];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float r = ref[b][e & 1];
+                x[b][e] = ex2(x[b][e] - (r == neg_inf() ? 0.f : r));
+              }
+              l[b][0] += x[b][0] + x[b][2];
+              l[b][1] += x[b][1] + x[b][3];
+              pf[b][0] = transpose8(pack2<BF16>(x[b][0], x[b][1]));
+              pf[b][1] = transpose8(pack2<BF16>(x[b][2], x[b][3]));
+            }
+            // O^T += V^T P^T
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              uint32_t a[4];
+              ldsm4t(va + (s >> 2) * (kKT * 128) + voff[s & 3], a);
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16816<BF16>(acc[s][b], a, pf[b][0], pf[b][1]);
             }
           }
-          // online softmax; row i of this thread: s*[2i], s*[2i + 1]
-          uint32_t pf[4];
+          __syncwarp();
+          if (lane == 0) sm100::mbar_arrive(&empty[st]);
+        }
+        if (++st == C::kStages) {
+          st = 0;
+          par ^= 1u;
+        }
+      }
+    }
+    // ---- end of the piece: add the warps' accumulators, a buffer per group ----
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float x[4] = {s0[2 * i], s0[2 * i + 1], s1[2 * i], s1[2 * i + 1]};
-            const int c = key0 + 2 * t4;
-            const int kk[4] = {c, c + 1, c + 8, c + 9};
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = kk[e] >= lo[i] && kk[e] < hi[i] ? x[e] * p.scale_log2 : neg_inf();
-            float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            mx = fmaxf(mx, mrow[i]);
-            const float ref = mx == neg_inf() ? 0.f : mx;
-            const float corr = ex2(mrow[i] - ref);
-            mrow[i] = mx;
-            float sum = 0.f;
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[b][i] += __shfl_xor_sync(0xffffffffu, l[b][i], d);
+        if (g == 0) {
+          wm[warp][8 * b + 2 * t4 + i] = ref[b][i];
+          wl[warp][8 * b + 2 * t4 + i] = l[b][i];
+        }
+      }
+    bar_consumers<kWarps>();
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * b + 2 * t4 + i;
+        float m = wm[0][r];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) m = fmaxf(m, wm[w][r]);
+        const float f = ex2(ref[b][i] - (m == neg_inf() ? 0.f : m));
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          acc[s][b][i] *= f;
+          acc[s][b][i + 2] *= f;
+        }
+      }
+    float* mg = merge + group * (kM * C::kPitch);
+    for (int w = 0; w < 4; ++w) {  // in warp order: the same sum every time
+      if (quarter == w) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              x[e] = ex2(x[e] - ref);
-              sum += x[e];
+              float* d = mg + (8 * b + 2 * t4 + (e & 1)) * C::kPitch + 16 * s + g + (e >> 1) * 8;
+              *d = w ? *d + acc[s][b][e] : acc[s][b][e];
             }
-            lrow[i] = fmaf(lrow[i], corr, sum);
-            pf[i] = pack2<BF16>(x[0], x[1]);
-            pf[i + 2] = pack2<BF16>(x[2], x[3]);
-            if (__any_sync(0xffffffffu, corr != 1.f)) {
-#pragma unroll
-              for (int c2 = 0; c2 < NT; ++c2) {
-                acc[c2][2 * i] *= corr;
-                acc[c2][2 * i + 1] *= corr;
-              }
-            }
-          }
-          // O += P V
-          const uint32_t vb = sm100::smem_u32(vt);
-          const int vrow = warp * 16 + (lane & 15);
-#pragma unroll
-          for (int c = 0; c < NT; c += 2) {
-            if (c * 8 < p.D) {
-              uint32_t b[4];
-              ldsm4t(vb + tile_at(vrow, c + (lane >> 4)), b);
-              mma16816<BF16>(acc[c], pf, b[0], b[1]);
-              mma16816<BF16>(acc[c + 1], pf, b[2], b[3]);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) sm100::mbar_arrive(&empty[st]);
       }
-    }
-    // ---- end of the piece: add the four warps' accumulators ----
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 1);
-      lrow[i] += __shfl_xor_sync(0xffffffffu, lrow[i], 2);
-      if (t4 == 0) {
-        wm[warp][g + 8 * i] = mrow[i];
-        wl[warp][g + 8 * i] = lrow[i];
-      }
-    }
-    bar_consumers();
-    float mall[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = g + 8 * i;
-      float m = wm[0][r];
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, wm[w][r]);
-      mall[i] = m;
-      const float f = ex2(mrow[i] - (m == neg_inf() ? 0.f : m));
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        acc[c][2 * i] *= f;
-        acc[c][2 * i + 1] *= f;
-      }
-    }
-    for (int w = 0; w < kWarps; ++w) {  // in warp order: the same sum every time
-      if (warp == w) {
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float2* d = reinterpret_cast<float2*>(merge + (g + 8 * i) * C::kPitch + c * 8 + 2 * t4);
-            float2 v = make_float2(acc[c][2 * i], acc[c][2 * i + 1]);
-            if (w) {
-              const float2 old = *d;
-              v.x += old.x;
-              v.y += old.y;
-            }
-            *d = v;
-          }
-      }
-      bar_consumers();
+      bar_consumers<kWarps>();
     }
     const bool whole = o.whole();
     const int slot = o.j0 > o.T0 ? 0 : 1;
@@ -313,69 +371,85 @@ __global__ void __launch_bounds__(kThreads, DecodeCfg<DP>::kCtasPerSm)
     for (int i = tid; i < kM * kLanesPerRow; i += kWarps * 32) {
       const int r = i / kLanesPerRow, c = (i % kLanesPerRow) * 8;
       if (r >= o.rows) break;
-      float m = wm[0][r], l = 0.f;
+      float m = wm[0][r], lsum = 0.f;
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) m = fmaxf(m, wm[w][r]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) l = fmaf(wl[w][r], ex2(wm[w][r] - (m == neg_inf() ? 0.f : m)), l);
+      for (int w = 0; w < kWarps; ++w) lsum = fmaf(wl[w][r], ex2(wm[w][r] - (m == neg_inf() ? 0.f : m)), lsum);
+      float v[8];
       const float* src = merge + r * C::kPitch + c;
-      const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
+#pragma unroll
+      for (int q = 0; q < 8; q += 4) {
+        const float4 a = *reinterpret_cast<const float4*>(src + q);
+        float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (kGroups == 2) b = *reinterpret_cast<const float4*>(src + kM * C::kPitch + q);
+        v[q] = a.x + b.x;
+        v[q + 1] = a.y + b.y;
+        v[q + 2] = a.z + b.z;
+        v[q + 3] = a.w + b.w;
+      }
       if (whole) {
         const int64_t row = attn_out_row(p, o.s.t0, o.h, o.row0 + r);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
         if (c < p.D) {
-          uint4 v;
-          v.x = pack2<BF16>(a.x * inv, a.y * inv);
-          v.y = pack2<BF16>(a.z * inv, a.w * inv);
-          v.z = pack2<BF16>(b.x * inv, b.y * inv);
-          v.w = pack2<BF16>(b.z * inv, b.w * inv);
-          *reinterpret_cast<uint4*>(p.out + row * p.D + c) = v;
+          uint4 u;
+          u.x = pack2<BF16>(v[0] * inv, v[1] * inv);
+          u.y = pack2<BF16>(v[2] * inv, v[3] * inv);
+          u.z = pack2<BF16>(v[4] * inv, v[5] * inv);
+          u.w = pack2<BF16>(v[6] * inv, v[7] * inv);
+          *reinterpret_cast<uint4*>(p.out + row * p.D + c) = u;
         }
-        if (c == 0 && p.lse) p.lse[row] = attn_lse(m, l);
+        if (c == 0 && p.lse) p.lse[row] = attn_lse(m, lsum);
       } else {
         float* dst = p.part + (pbase + r) * DP + c;
-        *reinterpret_cast<float4*>(dst) = a;
-        *reinterpret_cast<float4*>(dst + 4) = b;
-        if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (pbase + r) * 2) = make_float2(m, l);
+        *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(dst + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        if (c == 0) *reinterpret_cast<float2*>(p.part_ml + (pbase + r) * 2) = make_float2(m, lsum);
       }
     }
-    if (tid == 0) {
-      if (o.j0 == o.T0 && !whole) {
-        attn_write_desc(p, blockIdx.x, attn_last_cta(blockIdx.x, share, o), &o);
-        begun = true;
-      }
+    if (tid == 0 && o.j0 == o.T0 && !whole) {
+      attn_write_desc(p, blockIdx.x, attn_last_cta(blockIdx.x, share, o), &o);
+      begun = true;
     }
-    bar_consumers();  // wm, wl and merge are free again
+    bar_consumers<kWarps>();  // wm, wl and merge are free again
   }
   if (tid == 0 && !begun && start.units > 0) attn_write_desc(p, blockIdx.x, 0, nullptr);
 }
 
-int g_conf[2][4][64];
+int g_conf[2][4][2][64];
+
+template <bool BF16, int DP, int NB>
+cudaError_t run(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s, int ctas) {
+  using C = DecodeCfg<DP, NB>;
+  auto* kernel = attn_decode_kernel<BF16, DP, NB>;
+  const cudaError_t e = smem_attr_once(kernel, C::kSmem, g_conf[BF16][DP / 64 - 1][NB - 1]);
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, C::kThreads, C::kSmem, s>>>(k, v, p);
+  return cudaGetLastError();
+}
 
 template <bool BF16, int DP>
-cudaError_t run(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s, int ctas) {
-  auto* kernel = attn_decode_kernel<BF16, DP>;
-  const cudaError_t e = smem_attr_once(kernel, DecodeCfg<DP>::kSmem, g_conf[BF16][DP / 64 - 1]);
-  if (e != cudaSuccess) return e;
-  kernel<<<ctas, kThreads, DecodeCfg<DP>::kSmem, s>>>(k, v, p);
-  return cudaGetLastError();
+cudaError_t run(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s, int ctas, int m) {
+  return m == 8 ? run<BF16, DP, 1>(p, k, v, s, ctas) : run<BF16, DP, 2>(p, k, v, s, ctas);
 }
 
 }  // namespace
 
-int attn_decode_ctas(const AttnParams& p, int sms) { return (attn_padded(p.D) <= 128 ? 2 : 1) * sms; }
+int attn_decode_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
+
+int attn_decode_ctas(int D, int sms) { return (attn_padded(D) <= 128 ? 2 : 1) * sms; }
 
 cudaError_t launch_attn_decode(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s,
-                               int ctas) {
+                               int ctas, int m) {
   switch (attn_padded(p.D) / 64 * 2 + (p.bf16 ? 1 : 0)) {
-    case 2: return run<false, 64>(p, k, v, s, ctas);
-    case 3: return run<true, 64>(p, k, v, s, ctas);
-    case 4: return run<false, 128>(p, k, v, s, ctas);
-    case 5: return run<true, 128>(p, k, v, s, ctas);
-    case 6: return run<false, 192>(p, k, v, s, ctas);
-    case 7: return run<true, 192>(p, k, v, s, ctas);
-    case 8: return run<false, 256>(p, k, v, s, ctas);
-    default: return run<true, 256>(p, k, v, s, ctas);
+    case 2: return run<false, 64>(p, k, v, s, ctas, m);
+    case 3: return run<true, 64>(p, k, v, s, ctas, m);
+    case 4: return run<false, 128>(p, k, v, s, ctas, m);
+    case 5: return run<true, 128>(p, k, v, s, ctas, m);
+    case 6: return run<false, 192>(p, k, v, s, ctas, m);
+    case 7: return run<true, 192>(p, k, v, s, ctas, m);
+    case 8: return run<false, 256>(p, k, v, s, ctas, m);
+    default: return run<true, 256>(p, k, v, s, ctas, m);
   }
 }
 
