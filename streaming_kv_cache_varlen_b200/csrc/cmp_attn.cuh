@@ -127,19 +127,30 @@ __device__ __forceinline__ void attn_tiles(int lo, int hi, int& T0, int& T1) {
 // (compressed rows of a prompt: 322 us).
 constexpr int kItemCost = 3;
 
-// A CTA's way along its part of the line. `m` rows per item.
-template <int KT>
+// Row tiles of one key head of a sequence.
+template <int M>
+__device__ __forceinline__ int attn_row_tiles(const AttnParams& p, const AttnSeq& s) {
+  return (int)(((uint32_t)s.len * (uint32_t)p.G + (M - 1)) / M);  // T * Hq <= INT32_MAX
+}
+
+// n / d, in 32 bits where they suffice (a 64-bit division takes half a microsecond).
+__device__ __forceinline__ int64_t attn_div64(int64_t n, int64_t d) {
+  if (((n | d) >> 32) == 0) return (int64_t)((uint32_t)n / (uint32_t)d);
+  return n / d;
+}
+
+// A CTA's way along its part of the line. M rows per item.
+template <int KT, int M>
 struct AttnWalk {
   const AttnParams& p;
-  int m;
   int64_t left;  // units still to do
   int b, h, qt, off;
   int nq;
   AttnSeq s;
-  __device__ __forceinline__ AttnWalk(const AttnParams& p_, int m_) : p(p_), m(m_) {}
+  __device__ __forceinline__ AttnWalk(const AttnParams& p_) : p(p_) {}
   __device__ __forceinline__ void open() {
     s = attn_seq(p, b);
-    nq = (int)(((int64_t)s.len * p.G + m - 1) / m);
+    nq = attn_row_tiles<M>(p, s);
   }
   __device__ __forceinline__ void begin(int64_t units, int b_, int h_, int qt_, int off_) {
     left = units;
@@ -163,8 +174,8 @@ struct AttnWalk {
       o.s = s;
       o.b = b;
       o.h = h;
-      o.row0 = qt * m;
-      o.rows = min(m, s.len * p.G - o.row0);
+      o.row0 = qt * M;
+      o.rows = min(M, s.len * p.G - o.row0);
       attn_range(p, s, o.row0, o.rows, o.lo, o.hi);
       attn_tiles<KT>(o.lo, o.hi, o.T0, o.T1);
       const int n = o.T1 - o.T0 + kItemCost;
@@ -190,23 +201,23 @@ struct AttnStart {
 };
 
 // Units of row tile qt of one key head of sequence s.
-template <int KT>
-__device__ __forceinline__ int attn_tile_units(const AttnParams& p, const AttnSeq& s, int m, int qt) {
+template <int KT, int M>
+__device__ __forceinline__ int attn_tile_units(const AttnParams& p, const AttnSeq& s, int qt) {
   int lo, hi, T0, T1;
-  const int r = qt * m;
-  attn_range(p, s, r, min(m, s.len * p.G - r), lo, hi);
+  const int r = qt * M;
+  attn_range(p, s, r, min(M, s.len * p.G - r), lo, hi);
   attn_tiles<KT>(lo, hi, T0, T1);
   return T1 - T0 + kItemCost;
 }
 
 // Units of one key head of each lane's sequence, by the whole warp: sequences of
 // few row tiles by their own lane, the others by all lanes one after another.
-template <int KT>
-__device__ __forceinline__ int64_t attn_head_units(const AttnParams& p, const AttnSeq& s, int m, int lane) {
-  const int nq = (int)(((int64_t)s.len * p.G + m - 1) / m);
+template <int KT, int M>
+__device__ __forceinline__ int64_t attn_head_units(const AttnParams& p, const AttnSeq& s, int lane) {
+  const int nq = attn_row_tiles<M>(p, s);
   int64_t n = 0;
   if (nq <= 4)
-    for (int qt = 0; qt < nq; ++qt) n += attn_tile_units<KT>(p, s, m, qt);
+    for (int qt = 0; qt < nq; ++qt) n += attn_tile_units<KT, M>(p, s, qt);
   for (unsigned big = __ballot_sync(0xffffffffu, nq > 4); big; big &= big - 1) {
     const int src = __ffs(big) - 1;
     AttnSeq t;
@@ -214,7 +225,7 @@ __device__ __forceinline__ int64_t attn_head_units(const AttnParams& p, const At
     t.start = __shfl_sync(0xffffffffu, s.start, src);
     const int tq = __shfl_sync(0xffffffffu, nq, src);
     int64_t part = 0;
-    for (int qt = lane; qt < tq; qt += 32) part += attn_tile_units<KT>(p, t, m, qt);
+    for (int qt = lane; qt < tq; qt += 32) part += attn_tile_units<KT, M>(p, t, qt);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
     if (lane == src) n = part;
@@ -225,9 +236,8 @@ __device__ __forceinline__ int64_t attn_head_units(const AttnParams& p, const At
 // Every thread sums its run of consecutive sequences, the block scans the sums,
 // and the warp whose run holds the part's first unit walks to it. *err gets
 // kErrIndex from CTA 0 if a sequence is not usable. Ends with __syncthreads.
-template <int KT, int NT>
-__device__ __forceinline__ void attn_plan(const AttnParams& p, int m, AttnStart* st, int64_t* warp_sum,
-                                          unsigned* err) {
+template <int KT, int M, int NT>
+__device__ __forceinline__ void attn_plan(const AttnParams& p, AttnStart* st, int64_t* warp_sum, unsigned* err) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + NT - 1) / NT;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -239,7 +249,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int m, AttnStart*
     s.bad = false;
     if (b0 + i < b1) s = attn_seq(p, b0 + i);
     bad |= s.bad;
-    sum += attn_head_units<KT>(p, s, m, lane) * p.Hk;
+    sum += attn_head_units<KT, M>(p, s, lane) * p.Hk;
   }
   if (bad && blockIdx.x == 0) atomicOr(err, kErrIndex);
   int64_t inc = sum;
@@ -258,7 +268,7 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int m, AttnStart*
     total += warp_sum[w];
   }
   base += inc - sum;
-  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t share = attn_div64(total + gridDim.x - 1, gridDim.x);
   int64_t u = (int64_t)blockIdx.x * share;
   // the warp whose run holds unit u walks to it, 32 row tiles at a time
   const unsigned owner = __ballot_sync(0xffffffffu, u < total && u >= base && u < base + sum);
@@ -268,19 +278,19 @@ __device__ __forceinline__ void attn_plan(const AttnParams& p, int m, AttnStart*
     int64_t v = u - __shfl_sync(0xffffffffu, base, src);
     for (int b = sb0; b < sb1; ++b) {
       const AttnSeq s = attn_seq(p, b);
-      const int nq = (int)(((int64_t)s.len * p.G + m - 1) / m);
+      const int nq = attn_row_tiles<M>(p, s);
       int64_t hu = 0;
-      for (int qt = lane; qt < nq; qt += 32) hu += attn_tile_units<KT>(p, s, m, qt);
+      for (int qt = lane; qt < nq; qt += 32) hu += attn_tile_units<KT, M>(p, s, qt);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) hu += __shfl_xor_sync(0xffffffffu, hu, o);
       if (v >= hu * p.Hk) {
         v -= hu * p.Hk;
         continue;
       }
-      const int h = (int)(v / hu);
+      const int h = (int)attn_div64(v, hu);
       v -= h * hu;
       for (int qt0 = 0;; qt0 += 32) {
-        const int n = qt0 + lane < nq ? attn_tile_units<KT>(p, s, m, qt0 + lane) : 0;
+        const int n = qt0 + lane < nq ? attn_tile_units<KT, M>(p, s, qt0 + lane) : 0;
         int64_t c = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -317,7 +327,7 @@ __device__ __forceinline__ void attn_write_desc(const AttnParams& p, int cta, in
 // The last CTA of the item of a piece that its CTA does not end: `rest` tiles
 // follow, the next CTAs do `share` each.
 __device__ __forceinline__ int attn_last_cta(int cta, int64_t share, const AttnPiece& o) {
-  return cta + (int)((o.T1 - o.j1 + share - 1) / share);
+  return cta + (int)attn_div64(o.T1 - o.j1 + share - 1, share);
 }
 
 // Row r of a piece's item -> the row of out / lse ([T * Hq]).

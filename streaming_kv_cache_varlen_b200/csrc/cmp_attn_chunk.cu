@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 8) sm100::tmem_alloc(&tmem_slot, 512);
   sm100::tc_fence_before();
-  attn_plan<KT, kThreads>(p, C::kM, &start, warp_sum, &g_attn_err);  // ends with __syncthreads
+  attn_plan<KT, C::kM, kThreads>(p, &start, warp_sum, &g_attn_err);  // ends with __syncthreads
   sm100::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   // Piece i of this CTA, when the scheduler has written it (its .valid is false
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::regs_dec<kOtherRegs>();
     if (warp == 10) {  // ---- scheduler: the pieces of this CTA's part, a few ahead ----
       if (lane == 0) {
-        AttnWalk<KT> walk(p, C::kM);
+        AttnWalk<KT, C::kM> walk(p);
         walk.begin(start.units, start.b, start.h, start.qt, start.off);
         const int64_t share = start.share;
         for (int i = 0;; ++i) {

@@ -106,8 +106,8 @@ __global__ void __launch_bounds__(DecodeCfg<DP, NB>::kThreads, DecodeCfg<DP, NB>
     }
     sm100::fence_barrier_init();
   }
-  attn_plan<kKT, kThreads>(p, kM, &start, warp_sum, &g_attn_err);
-  AttnWalk<kKT> walk(p, kM);
+  attn_plan<kKT, kM, kThreads>(p, &start, warp_sum, &g_attn_err);
+  AttnWalk<kKT, kM> walk(p);
   walk.begin(start.units, start.b, start.h, start.qt, start.off);
   const int64_t share = start.share;
 
@@ -464,7 +464,7 @@ bool attn_cache_map(CUtensorMap* m, const void* cache, const AttnParams& p) {
   const cuuint32_t estr[3] = {1, 1, 1};
   return f(m, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
            const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
