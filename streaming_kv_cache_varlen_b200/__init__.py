@@ -273,66 +273,99 @@ def nsa_compress(input, weight, slot_mapping, act_seq_len, output_cache, *, comp
 
 
 _ROPE_PAIRS = {"interleaved": 0, "halves": 1}
-_DTYPE = {}  # torch dtype -> CMP_NSA_FP16 / CMP_NSA_BF16, filled on first use
+_torch = None
+_DTYPE = {}  # torch dtype -> CMP_NSA_FP16 / CMP_NSA_BF16
 
 
-def _dtype16(t, name) -> int:
-    import torch
-    if not _DTYPE:
+# The paged operators' calls are short (a decode step's append takes 3 us on the device), so
+# their checks look at each tensor once, without torch.device objects and without entering a
+# device context when the tensors are on the current device; what fails a check is described by
+# _check and _check_tokens.
+
+def _torch_module():
+    global _torch
+    if _torch is None:
+        import torch
         _DTYPE.update({torch.float16: 0, torch.bfloat16: 1})
+        _torch = torch
+    return _torch
+
+
+def _dtype16(t, name, torch) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must be on a CUDA device")
-    if t.dtype not in _DTYPE:
+    dt = _DTYPE.get(t.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be float16 or bfloat16")
-    return _DTYPE[t.dtype]
+    return dt
 
 
-def _check_tokens(t, name, dtype, shape, device) -> int:
+def _dense(t, name, dtype, dim, dev, idx, torch):
+    """_check, quickly."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == idx and t.dim() == dim
+            and t.is_contiguous()):
+        _check(t, name, dtype, dim, dev)
+
+
+def _check_tokens(t, name, dtype, T, H, D, dev, idx, torch) -> int:
     """[T, H, D] with the last two dimensions dense; returns the token stride in elements."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or tuple(t.shape[1:]) != tuple(shape[1:]) or (shape[0] is not None and t.shape[0] != shape[0]):
-        raise ValueError(f"{name} must be {['T' if s is None else s for s in shape]}, got {list(t.shape)}")
-    H, D = t.shape[1], t.shape[2]
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    if t.shape != (T, H, D):
+        raise ValueError(f"{name} must be {[T, H, D]}, got {list(t.shape)}")
+    st, sh, sd = t.stride()
+    if (D > 1 and sd != 1) or (H > 1 and sh != D):
         raise ValueError(f"the last two dimensions of {name} must be dense")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    stride = t.stride(0) if t.shape[0] > 1 else H * D
-    if stride < H * D or stride % 8 or t.data_ptr() % 16:
+    if t.get_device() != idx:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if T <= 1:
+        st = H * D
+    if st < H * D or st % 8 or t.data_ptr() % 16:
         raise ValueError(f"{name}: tokens must start on 16-byte boundaries, {H * D} or more elements apart")
-    return stride
+    return st
 
 
-def _rope(sin, cos, pairs, T, D, device):
+def _rope(sin, cos, pairs, T, D, dev, idx, torch):
     """cmp_rope of the tables, or None."""
-    import torch
-    if pairs not in _ROPE_PAIRS:
+    kind = _ROPE_PAIRS.get(pairs)
+    if kind is None:
         raise ValueError(f"rope_pairs must be one of {sorted(_ROPE_PAIRS)}")
     if sin is None and cos is None:
         return None
     if sin is None or cos is None:
         raise ValueError("sin and cos come together")
-    if sin.dtype not in (torch.float32, torch.bfloat16):
+    dt = sin.dtype
+    if dt != torch.float32 and dt != torch.bfloat16:
         raise TypeError("sin and cos must be float32 or bfloat16")
-    for t, name in ((sin, "sin"), (cos, "cos")):
-        _check(t, name, sin.dtype, 2, device)
-    R = sin.shape[1]
-    if tuple(sin.shape) != (T, R) or sin.shape != cos.shape or R < 16 or R % 16 or R > D:
+    _dense(sin, "sin", dt, 2, dev, idx, torch)
+    _dense(cos, "cos", dt, 2, dev, idx, torch)
+    n, R = sin.shape
+    if n != T or cos.shape != sin.shape or R < 16 or R % 16 or R > D:
         raise ValueError(f"sin and cos must both be [{T}, dim] with dim a multiple of 16, at most {D}")
-    return cmp_rope(_ptr(sin), _ptr(cos), R, _ROPE_PAIRS[pairs], 0 if sin.dtype == torch.float32 else 1)
+    return ctypes.byref(cmp_rope(sin.data_ptr(), cos.data_ptr(), R, kind, 0 if dt == torch.float32 else 1))
 
 
-def _handle(stream, dev):
-    import torch
+def _handle(stream, idx, torch):
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        return torch._C._cuda_getCurrentRawStream(idx)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_stream(handle, dev, torch):
+    """Context in which tensors are allocated that belong to the stream `handle`."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, dev))
+
+
+def _on_device(idx, torch, call, *args):
+    """call(*args) with device idx current."""
+    if torch._C._cuda_getDevice() == idx:
+        return call(*args)
+    with torch.cuda.device(idx):
+        return call(*args)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight=None, *, sin=None, cos=None, rope_pairs: str = "interleaved",
@@ -345,62 +378,65 @@ def qk_norm_rope(q, k, q_weight, k_weight=None, *, sin=None, cos=None, rope_pair
     channels of a head are rotated; None: no rotation), ``rope_pairs`` "interleaved"
     (channels 2j, 2j+1) or "halves" (j, dim/2 + j). ``q_out`` / ``k_out`` may be q / k
     (in place); new dense tensors by default."""
-    import torch
-    dt = _dtype16(q, "q")
-    dev = q.device
+    torch = _torch_module()
+    dt = _dtype16(q, "q", torch)
+    dev, idx, dtype = q.device, q.get_device(), q.dtype
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D]")
     T, Hq, D = q.shape
-    qs = _check_tokens(q, "q", q.dtype, (T, Hq, D), dev)
-    _check(q_weight, "q_weight", q.dtype, 1, dev)
+    qs = _check_tokens(q, "q", dtype, T, Hq, D, dev, idx, torch)
+    _dense(q_weight, "q_weight", dtype, 1, dev, idx, torch)
     Hk = ks = kos = 0
+    kp = kwp = kop = None
     if k is not None:
         if not isinstance(k, torch.Tensor) or k.dim() != 3 or k_weight is None:
             raise ValueError("k must be [T, Hk, D] and comes with k_weight")
         Hk = k.shape[1]
-        ks = _check_tokens(k, "k", q.dtype, (T, Hk, D), dev)
-        _check(k_weight, "k_weight", q.dtype, 1, dev)
+        ks = _check_tokens(k, "k", dtype, T, Hk, D, dev, idx, torch)
+        _dense(k_weight, "k_weight", dtype, 1, dev, idx, torch)
+        kp, kwp = k.data_ptr(), k_weight.data_ptr()
     if q_weight.shape[0] != D or (k is not None and k_weight.shape[0] != D):
         raise ValueError(f"the weights must be [{D}]")
-    rope = _rope(sin, cos, rope_pairs, T, D, dev)
-    handle = _handle(stream, dev)
-    if (q_out is None or (k is not None and k_out is None)) and stream is not None:
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, dev)):
-            q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if q_out is None else q_out
-            k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev) if k is not None and k_out is None else k_out
-    else:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if q_out is None else q_out
-        k_out = torch.empty((T, Hk, D), dtype=q.dtype, device=dev) if k is not None and k_out is None else k_out
-    qos = _check_tokens(q_out, "q_out", q.dtype, (T, Hq, D), dev)
+    rope = _rope(sin, cos, rope_pairs, T, D, dev, idx, torch)
+    handle = _handle(stream, idx, torch)
+    need_q, need_k = q_out is None, k is not None and k_out is None
+    if need_q or need_k:
+        if stream is None:
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev) if need_q else q_out
+            k_out = torch.empty((T, Hk, D), dtype=dtype, device=dev) if need_k else k_out
+        else:
+            with _on_stream(handle, dev, torch):
+                q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev) if need_q else q_out
+                k_out = torch.empty((T, Hk, D), dtype=dtype, device=dev) if need_k else k_out
+    qos = Hq * D if need_q else _check_tokens(q_out, "q_out", dtype, T, Hq, D, dev, idx, torch)
     if k is not None:
-        kos = _check_tokens(k_out, "k_out", q.dtype, (T, Hk, D), dev)
-    dims = cmp_qk_dims(T, Hq, Hk, D, qs, ks, qos, kos)
-    with torch.cuda.device(dev):
-        st = lib.cmp_qk_norm_rope(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight) if k is not None else None,
-                                  None if rope is None else ctypes.byref(rope), eps, dt, _ptr(q_out),
-                                  _ptr(k_out) if k is not None else None, handle, ctypes.byref(dims))
+        kos = Hk * D if need_k else _check_tokens(k_out, "k_out", dtype, T, Hk, D, dev, idx, torch)
+        kop = k_out.data_ptr()
+    st = _on_device(idx, torch, lib.cmp_qk_norm_rope, q.data_ptr(), kp, q_weight.data_ptr(), kwp, rope, eps, dt,
+                    q_out.data_ptr(), kop, handle, ctypes.byref(cmp_qk_dims(T, Hq, Hk, D, qs, ks, qos, kos)))
     if st != CMP_OK:
         raise CmpError(st, "cmp_qk_norm_rope")
     return q_out, (k_out if k is not None else None)
 
 
-def _check_cache(k_cache, v_cache, dtype, Hk, D, dev):
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _check(t, name, dtype, 4, dev)
-    if k_cache.shape != v_cache.shape or tuple(k_cache.shape[2:]) != (Hk, D):
+def _check_cache(k_cache, v_cache, dtype, Hk, D, dev, idx, torch):
+    _dense(k_cache, "k_cache", dtype, 4, dev, idx, torch)
+    _dense(v_cache, "v_cache", dtype, 4, dev, idx, torch)
+    shape = k_cache.shape
+    if shape != v_cache.shape or shape[2] != Hk or shape[3] != D:
         raise ValueError(f"k_cache and v_cache must both be [block_num, page_size, {Hk}, {D}]")
+    return shape
 
 
-def _check_sequences(block_table, cu_seqlens, start_pos, dev) -> int:
-    import torch
+def _check_sequences(block_table, cu_seqlens, start_pos, dev, idx, torch) -> int:
     i32 = torch.int32
-    _check(block_table, "block_table", i32, 2, dev)
-    _check(cu_seqlens, "cu_seqlens", i32, 1, dev)
+    _dense(block_table, "block_table", i32, 2, dev, idx, torch)
+    _dense(cu_seqlens, "cu_seqlens", i32, 1, dev, idx, torch)
     B = cu_seqlens.shape[0] - 1
     if B < 0 or block_table.shape[0] != B:
         raise ValueError("cu_seqlens must be [B + 1] and block_table [B, table_stride]")
     if start_pos is not None:
-        _check(start_pos, "start_pos", i32, 1, dev)
+        _dense(start_pos, "start_pos", i32, 1, dev, idx, torch)
         if start_pos.shape[0] != B:
             raise ValueError("start_pos must be [B]")
     return B
@@ -415,26 +451,25 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_seqlens, start_pos=None, *
     k, v [T, Hk, D] fp16 / bf16, last two dimensions dense; caches [block_num, page_size,
     Hk, D]; block_table int32 [B, pages]; cu_seqlens int32 [B+1]; start_pos int32 [B] or
     None; norm_weight [D]; sin / cos [T, dim] float32 or bf16, as for ``qk_norm_rope``."""
-    import torch
-    dt = _dtype16(k, "k")
-    dev = k.device
+    torch = _torch_module()
+    dt = _dtype16(k, "k", torch)
+    dev, idx, dtype = k.device, k.get_device(), k.dtype
     if k.dim() != 3:
         raise ValueError("k must be [T, Hk, D]")
     T, Hk, D = k.shape
-    ks = _check_tokens(k, "k", k.dtype, (T, Hk, D), dev)
-    vs = _check_tokens(v, "v", k.dtype, (T, Hk, D), dev)
-    _check_cache(k_cache, v_cache, k.dtype, Hk, D, dev)
-    B = _check_sequences(block_table, cu_seqlens, start_pos, dev)
+    ks = _check_tokens(k, "k", dtype, T, Hk, D, dev, idx, torch)
+    vs = _check_tokens(v, "v", dtype, T, Hk, D, dev, idx, torch)
+    shape = _check_cache(k_cache, v_cache, dtype, Hk, D, dev, idx, torch)
+    B = _check_sequences(block_table, cu_seqlens, start_pos, dev, idx, torch)
     if norm_weight is not None:
-        _check(norm_weight, "norm_weight", k.dtype, 1, dev)
+        _dense(norm_weight, "norm_weight", dtype, 1, dev, idx, torch)
         if norm_weight.shape[0] != D:
             raise ValueError(f"norm_weight must be [{D}]")
-    rope = _rope(sin, cos, rope_pairs, T, D, dev)
-    dims = cmp_kv_dims(B, T, Hk, D, ks, vs, k_cache.shape[0], k_cache.shape[1], block_table.shape[1])
-    with torch.cuda.device(dev):
-        st = lib.cmp_kv_append(_ptr(k), _ptr(v), _ptr(norm_weight), None if rope is None else ctypes.byref(rope), eps,
-                               _ptr(block_table), _ptr(cu_seqlens), _ptr(start_pos), dt, _ptr(k_cache),
-                               _ptr(v_cache), _handle(stream, dev), ctypes.byref(dims))
+    rope = _rope(sin, cos, rope_pairs, T, D, dev, idx, torch)
+    st = _on_device(idx, torch, lib.cmp_kv_append, k.data_ptr(), v.data_ptr(), _ptr(norm_weight), rope, eps,
+                    block_table.data_ptr(), cu_seqlens.data_ptr(), _ptr(start_pos), dt, k_cache.data_ptr(),
+                    v_cache.data_ptr(), _handle(stream, idx, torch),
+                    ctypes.byref(cmp_kv_dims(B, T, Hk, D, ks, vs, shape[0], shape[1], block_table.shape[1])))
     if st != CMP_OK:
         raise CmpError(st, "cmp_kv_append")
     return k_cache, v_cache
@@ -455,59 +490,59 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos=None
     keys a token sees at most; ``key_block`` / ``key_stride`` describe caches of compressed
     rows. ``workspace``: a CUDA tensor of at least ``paged_attention_workspace`` bytes
     (allocated per call by default)."""
-    import torch
-    dt = _dtype16(q, "q")
-    dev = q.device
+    torch = _torch_module()
+    dt = _dtype16(q, "q", torch)
+    dev, idx, dtype = q.device, q.get_device(), q.dtype
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D]")
     T, Hq, D = q.shape
-    qs = _check_tokens(q, "q", q.dtype, (T, Hq, D), dev)
+    qs = _check_tokens(q, "q", dtype, T, Hq, D, dev, idx, torch)
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [block_num, page_size, Hk, D]")
     Hk = k_cache.shape[2]
-    _check_cache(k_cache, v_cache, q.dtype, Hk, D, dev)
-    B = _check_sequences(block_table, cu_seqlens, start_pos, dev)
+    shape = _check_cache(k_cache, v_cache, dtype, Hk, D, dev, idx, torch)
+    B = _check_sequences(block_table, cu_seqlens, start_pos, dev, idx, torch)
     if max_len is not None and max_len < 1:
         raise ValueError("max_len must be at least 1")
     if window is not None and window < 1:
         raise ValueError("window must be at least 1")
     if scale is None:
         scale = D ** -0.5
-    dims = cmp_attn_dims(B, T, Hq, Hk, D, qs, k_cache.shape[0], k_cache.shape[1], block_table.shape[1], max_len or 0)
-    need = int(lib.cmp_paged_attention_workspace(ctypes.byref(dims)))
-    handle = _handle(stream, dev)
+    dims = ctypes.byref(cmp_attn_dims(B, T, Hq, Hk, D, qs, shape[0], shape[1], block_table.shape[1], max_len or 0))
+    handle = _handle(stream, idx, torch)
 
     def allocate():
-        return (torch.empty((T, Hq, D), dtype=q.dtype, device=dev) if out is None else out,
+        # 0 bytes for dimensions that the call below refuses
+        need = 0 if workspace is not None else _on_device(idx, torch, lib.cmp_paged_attention_workspace, dims)
+        return (torch.empty((T, Hq, D), dtype=dtype, device=dev) if out is None else out,
                 torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse is None and return_lse else lse,
                 torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace)
 
+    if out is not None:
+        _dense(out, "out", dtype, 3, dev, idx, torch)
+        if out.shape != (T, Hq, D):
+            raise ValueError(f"out must be [{T}, {Hq}, {D}]")
+    if lse is not None:
+        _dense(lse, "lse", torch.float32, 2, dev, idx, torch)
+        if lse.shape != (T, Hq):
+            raise ValueError(f"lse must be [{T}, {Hq}]")
+    if workspace is not None and (workspace.get_device() != idx or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the device of q")
     if stream is None:
         out, lse, workspace = allocate()
     else:  # memory that belongs to the stream the call runs on
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, dev)):
+        with _on_stream(handle, dev, torch):
             out, lse, workspace = allocate()
-    _check(out, "out", q.dtype, 3, dev)
-    if tuple(out.shape) != (T, Hq, D):
-        raise ValueError(f"out must be [{T}, {Hq}, {D}]")
-    if lse is not None:
-        _check(lse, "lse", torch.float32, 2, dev)
-        if tuple(lse.shape) != (T, Hq):
-            raise ValueError(f"lse must be [{T}, {Hq}]")
-    if workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the device of q")
-    with torch.cuda.device(dev):
-        st = lib.cmp_paged_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(cu_seqlens),
-                                     _ptr(start_pos), scale, window or 0, key_block, key_stride, dt, _ptr(out),
-                                     _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), handle,
-                                     ctypes.byref(dims))
+    st = _on_device(idx, torch, lib.cmp_paged_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                    block_table.data_ptr(), cu_seqlens.data_ptr(), _ptr(start_pos), scale, window or 0, key_block,
+                    key_stride, dt, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes, handle, dims)
     if st != CMP_OK:
         raise CmpError(st, "cmp_paged_attention")
     return out if lse is None else (out, lse)
 
 
 def paged_attention_workspace(T: int, Hq: int, Hk: int, D: int, max_len: Optional[int] = None) -> int:
-    """Bytes of ``workspace`` a ``paged_attention`` call of these sizes needs."""
+    """Bytes of ``workspace`` a ``paged_attention`` call of these sizes needs on the current device."""
     d = cmp_attn_dims(1, T, Hq, Hk, D, Hq * D, 1, 16, 1, max_len or 0)
     return int(lib.cmp_paged_attention_workspace(ctypes.byref(d)))
 
