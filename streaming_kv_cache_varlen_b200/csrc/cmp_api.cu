@@ -669,6 +669,7 @@ int cmp_kv_append(const void* k, const void* v, const void* norm_weight, const c
   p.Hk = (int)d.Hk;
   p.D = (int)d.D;
   p.page = (int)d.page_size;
+  p.div_page = cmp::make_fast_div(p.page);
   p.bf16 = dtype == CMP_NSA_BF16 ? 1 : 0;
   p.eps = eps;
   p.inv_d = 1.f / (float)d.D;

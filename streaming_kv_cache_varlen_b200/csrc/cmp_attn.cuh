@@ -27,27 +27,6 @@
 
 namespace cmp {
 
-// Division by a number that the host knows: n / d for 0 <= n < 2^31, 1 <= d < 2^31.
-// With s = ceil(log2 d) and mul = ceil(2^(31+s) / d) = (2^(31+s) + e) / d, 0 <= e < d <= 2^s,
-// the excess n e / (d 2^(31+s)) stays below 1 / d, so the floor is exact.
-struct FastDiv {
-  uint32_t mul;
-  int shift;
-  int d;
-#ifdef __CUDACC__
-  __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
-#endif
-};
-inline FastDiv make_fast_div(int d) {
-  FastDiv f;
-  int s = 0;
-  while (s < 31 && (int64_t(1) << s) < d) ++s;
-  f.shift = 31 + s;
-  f.mul = (uint32_t)((((uint64_t)1 << (31 + s)) + (uint32_t)d - 1) / (uint32_t)d);
-  f.d = d;
-  return f;
-}
-
 struct AttnParams {
   const uint16_t* q;         // token t at q + t * q_stride, its [Hq, D] dense
   const int32_t* table;      // [B, table_stride]

@@ -157,6 +157,27 @@ struct NsaParams {
   int64_t tokens, table_stride, result_len;
 };
 
+// Division by a number that the host knows: n / d for 0 <= n < 2^31, 1 <= d < 2^31.
+// With s = ceil(log2 d) and mul = ceil(2^(31+s) / d) = (2^(31+s) + e) / d, 0 <= e < d <= 2^s,
+// the excess n e / (d 2^(31+s)) stays below 1 / d, so the floor is exact.
+struct FastDiv {
+  uint32_t mul;
+  int shift;
+  int d;
+#ifdef __CUDACC__
+  __device__ __forceinline__ int div(int n) const { return (int)(((uint64_t)(uint32_t)n * mul) >> shift); }
+#endif
+};
+inline FastDiv make_fast_div(int d) {
+  FastDiv f;
+  int s = 0;
+  while (s < 31 && (int64_t(1) << s) < d) ++s;
+  f.shift = 31 + s;
+  f.mul = (uint32_t)((((uint64_t)1 << (31 + s)) + (uint32_t)d - 1) / (uint32_t)d);
+  f.d = d;
+  return f;
+}
+
 // The position rotation's tables: row t holds dim columns for token t.
 struct RopeTable {
   const void* sin;  // [T, dim] float32 (f32) or bf16
@@ -192,6 +213,7 @@ struct KvAppendParams {
   uint16_t* k_cache;         // [block_num, page, Hk, D]
   uint16_t* v_cache;
   int64_t T, k_stride, v_stride, table_stride, block_num;
+  FastDiv div_page;
   int B, Hk, D, page, bf16;
   float eps, inv_d;
 };

@@ -12,9 +12,11 @@
 // HBM bound: each element is read once and written once. A head's D channels
 // lie on LPH lanes of one warp, 8 consecutive channels (one 16-byte access) per
 // lane, so the sum of squares is log2(LPH) shuffles; a halves pair is exchanged
-// with the lane R/16 away, an interleaved pair stays inside the lane. A thread
-// keeps its token's table values and weights in registers and runs over the
-// token's heads, four heads' loads in flight at a time.
+// with the lane R/16 away, an interleaved pair stays inside the lane. A warp takes
+// a share of one token's heads, kUnroll heads per lane group with all their loads
+// in flight, and keeps the token's table values (16-byte loads) and the weights in
+// registers; for kv_append it looks up its token's cache row meanwhile, so a CTA
+// needs no barrier. KV_FIGURES
 #include "cmp_internal.cuh"
 
 #include <cuda_fp16.h>
@@ -23,7 +25,8 @@ namespace cmp {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;  // heads whose loads a thread has in flight
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 8;  // heads whose loads a thread has in flight
 
 __device__ unsigned g_kv_err;  // error word of kv_append on this device
 
@@ -59,9 +62,30 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ float rope_at(const RopeTable& r, const void* t, int64_t i) {
-  return r.f32 ? __ldg(static_cast<const float*>(t) + i)
-               : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(t) + i) << 16);
+// N (4 or 8) consecutive table values; i is a multiple of N.
+template <int N>
+__device__ __forceinline__ void rope_load(const RopeTable& r, const void* t, int64_t i, float (&f)[N]) {
+  if (r.f32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(t) + i);
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      const float4 v = __ldg(s + q);
+      f[4 * q] = v.x;
+      f[4 * q + 1] = v.y;
+      f[4 * q + 2] = v.z;
+      f[4 * q + 3] = v.w;
+    }
+  } else {
+    const uint2* s = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(t) + i);
+#pragma unroll
+    for (int q = 0; q < N / 4; ++q) {
+      const uint2 v = __ldg(s + q);
+      f[4 * q] = __uint_as_float(v.x << 16);
+      f[4 * q + 1] = __uint_as_float(v.x & 0xFFFF0000u);
+      f[4 * q + 2] = __uint_as_float(v.y << 16);
+      f[4 * q + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+  }
 }
 
 // A lane's part of its token's rotation: y[e] = x[e] * c[e] + partner[e] * s[e]
@@ -84,19 +108,24 @@ __device__ __forceinline__ void load_rope(const RopeTable& r, int64_t token, int
   if (r.halves) {
     const bool second = k >= R / 2;
     o.partner = second ? lane - R / 16 : lane + R / 16;
+    rope_load<8>(r, r.cos, row + k, o.c);
+    rope_load<8>(r, r.sin, row + k, o.s);
+    if (!second) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      o.c[e] = rope_at(r, r.cos, row + k + e);
-      const float s = rope_at(r, r.sin, row + k + e);
-      o.s[e] = second ? s : -s;
+      for (int e = 0; e < 8; ++e) o.s[e] = -o.s[e];
     }
   } else {
+    float ca[4], cb[4], sa[4], sb[4];
+    rope_load<4>(r, r.cos, row + k / 2, ca);
+    rope_load<4>(r, r.cos, row + R / 2 + k / 2, cb);
+    rope_load<4>(r, r.sin, row + k / 2, sa);
+    rope_load<4>(r, r.sin, row + R / 2 + k / 2, sb);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      o.c[2 * e] = rope_at(r, r.cos, row + k / 2 + e);
-      o.s[2 * e] = -rope_at(r, r.sin, row + k / 2 + e);
-      o.c[2 * e + 1] = rope_at(r, r.cos, row + R / 2 + k / 2 + e);
-      o.s[2 * e + 1] = rope_at(r, r.sin, row + R / 2 + k / 2 + e);
+      o.c[2 * e] = ca[e];
+      o.c[2 * e + 1] = cb[e];
+      o.s[2 * e] = -sa[e];
+      o.s[2 * e + 1] = sb[e];
     }
   }
 }
@@ -133,27 +162,27 @@ __device__ __forceinline__ void norm_rope(float (&x)[8], bool normed, const uint
   }
 }
 
-// Grid (tokens, head splits). The heads of a token (queries, then keys) go
-// round the groups of LPH lanes of its gridDim.y CTAs.
+// Grid (token quadruples, head splits): warp w of CTA (x, y) takes share y of the
+// heads (queries, then keys) of token 4 x + w.
 template <bool BF16, int LPH>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormParams p) {
-  const int64_t t = blockIdx.x;
-  const int lane = threadIdx.x % LPH;
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormParams p, int share) {
+  constexpr int kGroups = 32 / LPH;
+  const int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const int lane = threadIdx.x % LPH, g = (threadIdx.x & 31) / LPH;
   const int c0 = lane * 8;
   const bool live = c0 < p.D;
-  const int groups = (kThreads / LPH) * gridDim.y;
-  const int g = blockIdx.y * (kThreads / LPH) + threadIdx.x / LPH;
-  const int heads = p.Hq + p.Hk;
+  const int heads = min(p.Hq + p.Hk, ((int)blockIdx.y + 1) * share);
   const uint16_t* qrow = p.q + t * p.q_stride + c0;
   const uint16_t* krow = p.k + t * p.k_stride + c0;
   LaneRope lr;
   uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
   bool have = false;
-  for (int h0 = 0; h0 < heads; h0 += groups * kUnroll) {
+  for (int h0 = blockIdx.y * share + g; h0 - g < heads; h0 += kGroups * kUnroll) {
     uint4 v[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * groups + g;
+      const int h = h0 + u * kGroups;
       v[u] = make_uint4(0, 0, 0, 0);
       if (live && h < heads)
         v[u] = *reinterpret_cast<const uint4*>(h < p.Hq ? qrow + (int64_t)h * p.D : krow + (int64_t)(h - p.Hq) * p.D);
@@ -168,8 +197,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormPara
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (h0 + u * groups >= heads) break;  // uniform: no group has a head left
-      const int h = h0 + u * groups + g;
+      const int h = h0 + u * kGroups;
+      if (h - g >= heads) break;  // uniform: no group of the warp has a head left
       float x[8];
       unpack8<BF16>(v[u], x);
       norm_rope<BF16, LPH>(x, true, h < p.Hq ? wq : wk, p.inv_d, p.eps, p.rope, lr, lane);
@@ -199,11 +228,13 @@ __device__ __forceinline__ int warp_find_seq(const int32_t* cu, int B, int t, in
   return lo;
 }
 
-// Grid (tokens + 1, head splits): CTA x < T stores token x (its keys, then its
-// values, go round the groups), the CTA at x = T checks cu_seqlens as a whole.
+// Grid (token quadruples + 1, head splits): warp w of CTA (x, y) stores share y of
+// the heads (keys, then values) of token 4 x + w; the last CTA of a row of the grid
+// checks cu_seqlens as a whole.
 template <bool BF16, int LPH>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParams p) {
-  if ((int64_t)blockIdx.x == p.T) {
+__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParams p, int share) {
+  constexpr int kGroups = 32 / LPH;
+  if (blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y == 0) {
       bool bad = threadIdx.x == 0 && __ldg(p.cu) != 0;
       for (int b = threadIdx.x; b < p.B; b += kThreads) {
@@ -214,57 +245,63 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
     }
     return;
   }
-  const int t = blockIdx.x;
+  if ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5) >= p.T) return;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int wl = threadIdx.x & 31;
-  const int lane = threadIdx.x % LPH;
+  const int lane = wl % LPH, g = wl / LPH;
   const int c0 = lane * 8;
   const bool live = c0 < p.D;
-  const int groups = (kThreads / LPH) * gridDim.y;
-  const int g = blockIdx.y * (kThreads / LPH) + threadIdx.x / LPH;
-  const int heads = 2 * p.Hk;
+  const int heads = min(2 * p.Hk, ((int)blockIdx.y + 1) * share);
   const uint16_t* krow = p.k + (int64_t)t * p.k_stride + c0;
   const uint16_t* vrow = p.v + (int64_t)t * p.v_stride + c0;
   // the first heads and the table row do not depend on the sequence: load them
   // while it is looked up
+  int h0 = blockIdx.y * share + g;
   uint4 v[kUnroll];
+  auto load = [&]() {
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int h = u * groups + g;
-    v[u] = make_uint4(0, 0, 0, 0);
-    if (live && h < heads)
-      v[u] = *reinterpret_cast<const uint4*>(h < p.Hk ? krow + (int64_t)h * p.D : vrow + (int64_t)(h - p.Hk) * p.D);
-  }
-  LaneRope lr;
-  load_rope(p.rope, t, lane, c0, p.D, lr);
-  uint4 wk = make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u * kGroups;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (live && h < heads)
+        v[u] = *reinterpret_cast<const uint4*>(h < p.Hk ? krow + (int64_t)h * p.D : vrow + (int64_t)(h - p.Hk) * p.D);
+    }
+  };
+  load();
   const bool normed = p.norm_weight != nullptr;
-  if (live && normed) wk = __ldg(reinterpret_cast<const uint4*>(p.norm_weight + c0));
+  LaneRope lr;
+  lr.on = false;
+  lr.partner = lane;
+  uint4 wk = make_uint4(0, 0, 0, 0);
+  if (h0 - g < p.Hk) {  // the share holds keys
+    load_rope(p.rope, t, lane, c0, p.D, lr);
+    if (live && normed) wk = __ldg(reinterpret_cast<const uint4*>(p.norm_weight + c0));
+  }
   const int b = warp_find_seq(p.cu, p.B, t, wl);
   const int c = __ldg(p.cu + b), e = __ldg(p.cu + b + 1);
   if (t < c || t >= e) return;  // behind the last sequence: nothing to store
   const int64_t pos = (int64_t)(p.start_pos ? __ldg(p.start_pos + b) : 0) + (t - c);
   int64_t row = -1;
   if (pos >= t - c && pos < INT32_MAX) {
-    const int64_t pg = pos / p.page;
+    const int pg = p.div_page.div((int)pos);
     if (pg < p.table_stride) {
       const int blk = __ldg(p.table + (int64_t)b * p.table_stride + pg);
-      if (blk >= 0 && blk < p.block_num) row = (int64_t)blk * p.page + pos % p.page;
+      if (blk >= 0 && blk < p.block_num) row = (int64_t)blk * p.page + ((int)pos - pg * p.page);
     }
   }
   if (row < 0) {
-    if (threadIdx.x == 0) atomicOr(&g_kv_err, kErrIndex);
+    if (wl == 0) atomicOr(&g_kv_err, kErrIndex);
     return;
   }
   uint16_t* kdst = p.k_cache + row * p.Hk * p.D + c0;
   uint16_t* vdst = p.v_cache + row * p.Hk * p.D + c0;
-  for (int h0 = 0;;) {
+  for (;;) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (h0 + u * groups >= heads) break;
-      const int h = h0 + u * groups + g;
+      const int h = h0 + u * kGroups;
+      if (h - g >= heads) break;
       uint4 o = v[u];
-      // the warp's first group decides whether any of its heads is a key
-      if (h0 + u * groups + (g - (wl / LPH)) < p.Hk) {
+      if (h - g < p.Hk) {  // the warp's first group decides whether any of its heads is a key
         float x[8];
         unpack8<BF16>(v[u], x);
         norm_rope<BF16, LPH>(x, normed, wk, p.inv_d, p.eps, p.rope, lr, lane);
@@ -273,37 +310,37 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
       if (live && h < heads)
         *reinterpret_cast<uint4*>(h < p.Hk ? kdst + (int64_t)h * p.D : vdst + (int64_t)(h - p.Hk) * p.D) = o;
     }
-    h0 += groups * kUnroll;
-    if (h0 >= heads) return;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * groups + g;
-      if (live && h < heads)
-        v[u] = *reinterpret_cast<const uint4*>(h < p.Hk ? krow + (int64_t)h * p.D : vrow + (int64_t)(h - p.Hk) * p.D);
-    }
+    h0 += kGroups * kUnroll;
+    if (h0 - g >= heads) return;
+    load();
   }
 }
 
-// CTAs per token: enough that a small call covers the SMs, never more than its
-// heads can feed.
-int head_splits(int64_t T, int heads, int lph, int sms) {
-  const int per_cta = kThreads / lph;
-  const int most = (heads + per_cta - 1) / per_cta;
-  int64_t want = (2 * (int64_t)sms + T - 1) / (T > 0 ? T : 1);
-  return (int)(want < 1 ? 1 : want > most ? most : want);
+// Heads per warp: what its lane groups have in flight at once, fewer when the call
+// is too small to give every SM a few warps that way (a decode step).
+int head_share(int64_t T, int heads, int lph, int sms) {
+  const int groups = 32 / lph;
+  const int64_t warps = 8 * (int64_t)sms;  // wanted
+  int per_group = kUnroll;
+  while (per_group > 1 && T * ((heads + groups * per_group - 1) / (groups * per_group)) < warps) per_group /= 2;
+  const int splits = (heads + groups * per_group - 1) / (groups * per_group);
+  const int share = (heads + splits - 1) / splits;
+  return (share + groups - 1) / groups * groups;  // even shares of whole rounds of the groups
 }
 
 template <bool BF16, int LPH>
 cudaError_t run_norm(const QkNormParams& p, cudaStream_t s, int sms) {
-  const dim3 grid((unsigned)p.T, (unsigned)head_splits(p.T, p.Hq + p.Hk, LPH, sms));
-  qk_norm_rope_kernel<BF16, LPH><<<grid, kThreads, 0, s>>>(p);
+  const int heads = p.Hq + p.Hk, share = head_share(p.T, heads, LPH, sms);
+  const dim3 grid((unsigned)((p.T + kWarps - 1) / kWarps), (unsigned)((heads + share - 1) / share));
+  qk_norm_rope_kernel<BF16, LPH><<<grid, kThreads, 0, s>>>(p, share);
   return cudaGetLastError();
 }
 
 template <bool BF16, int LPH>
 cudaError_t run_append(const KvAppendParams& p, cudaStream_t s, int sms) {
-  const dim3 grid((unsigned)(p.T + 1), (unsigned)head_splits(p.T, 2 * p.Hk, LPH, sms));
-  kv_append_kernel<BF16, LPH><<<grid, kThreads, 0, s>>>(p);
+  const int heads = 2 * p.Hk, share = head_share(p.T, heads, LPH, sms);
+  const dim3 grid((unsigned)((p.T + kWarps - 1) / kWarps + 1), (unsigned)((heads + share - 1) / share));
+  kv_append_kernel<BF16, LPH><<<grid, kThreads, 0, s>>>(p, share);
   return cudaGetLastError();
 }
 
