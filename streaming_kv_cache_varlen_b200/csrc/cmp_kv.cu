@@ -15,7 +15,7 @@
 // with the lane R/16 away, an interleaved pair stays inside the lane. A warp takes
 // a share of one token's heads, kUnroll heads per lane group with all their loads
 // in flight, and keeps the token's table values (16-byte loads) and the weights in
-// registers; for kv_append it looks up its token's cache row meanwhile, so a CTA
+// registers, two batches in turn; for kv_append it looks up its token's cache row meanwhile, so a CTA
 // needs no barrier. KV_FIGURES
 #include "cmp_internal.cuh"
 
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 8;  // heads whose loads a thread has in flight
+constexpr int kUnroll = 4;  // heads a thread loads at once, while it computes as many others
 
 __device__ unsigned g_kv_err;  // error word of kv_append on this device
 
@@ -175,11 +175,7 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormPara
   const int heads = min(p.Hq + p.Hk, ((int)blockIdx.y + 1) * share);
   const uint16_t* qrow = p.q + t * p.q_stride + c0;
   const uint16_t* krow = p.k + t * p.k_stride + c0;
-  LaneRope lr;
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  bool have = false;
-  for (int h0 = blockIdx.y * share + g; h0 - g < heads; h0 += kGroups * kUnroll) {
-    uint4 v[kUnroll];
+  auto load = [&](uint4 (&v)[kUnroll], int h0) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * kGroups;
@@ -187,14 +183,20 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormPara
       if (live && h < heads)
         v[u] = *reinterpret_cast<const uint4*>(h < p.Hq ? qrow + (int64_t)h * p.D : krow + (int64_t)(h - p.Hq) * p.D);
     }
-    if (!have) {  // after the first heads' loads are on their way
-      have = true;
-      load_rope(p.rope, t, lane, c0, p.D, lr);
-      if (live) {
-        wq = __ldg(reinterpret_cast<const uint4*>(p.q_weight + c0));
-        if (p.Hk) wk = __ldg(reinterpret_cast<const uint4*>(p.k_weight + c0));
-      }
-    }
+  };
+  int h0 = blockIdx.y * share + g;
+  uint4 va[kUnroll], vb[kUnroll];
+  load(va, h0);
+  LaneRope lr;
+  load_rope(p.rope, t, lane, c0, p.D, lr);
+  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (live) {
+    wq = __ldg(reinterpret_cast<const uint4*>(p.q_weight + c0));
+    if (p.Hk) wk = __ldg(reinterpret_cast<const uint4*>(p.k_weight + c0));
+  }
+  uint16_t* qdst = p.q_out + t * p.qo_stride + c0;
+  uint16_t* kdst = p.k_out + t * p.ko_stride + c0;
+  auto store = [&](const uint4 (&v)[kUnroll], int h0) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * kGroups;
@@ -202,12 +204,21 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const QkNormPara
       float x[8];
       unpack8<BF16>(v[u], x);
       norm_rope<BF16, LPH>(x, true, h < p.Hq ? wq : wk, p.inv_d, p.eps, p.rope, lr, lane);
-      if (live && h < heads) {
-        uint16_t* o = h < p.Hq ? p.q_out + t * p.qo_stride + (int64_t)h * p.D
-                               : p.k_out + t * p.ko_stride + (int64_t)(h - p.Hq) * p.D;
-        *reinterpret_cast<uint4*>(o + c0) = pack8<BF16>(x);
-      }
+      if (live && h < heads)
+        *reinterpret_cast<uint4*>(h < p.Hq ? qdst + (int64_t)h * p.D : kdst + (int64_t)(h - p.Hq) * p.D) =
+            pack8<BF16>(x);
     }
+  };
+  constexpr int kStep = kGroups * kUnroll;
+  for (;;) {  // two buffers, so that a store's loads were issued a round before
+    if (h0 + kStep - g < heads) load(vb, h0 + kStep);
+    store(va, h0);
+    h0 += kStep;
+    if (h0 - g >= heads) return;
+    if (h0 + kStep - g < heads) load(va, h0 + kStep);
+    store(vb, h0);
+    h0 += kStep;
+    if (h0 - g >= heads) return;
   }
 }
 
@@ -257,8 +268,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
   // the first heads and the table row do not depend on the sequence: load them
   // while it is looked up
   int h0 = blockIdx.y * share + g;
-  uint4 v[kUnroll];
-  auto load = [&]() {
+  auto load = [&](uint4 (&v)[kUnroll], int h0) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * kGroups;
@@ -267,7 +277,10 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
         v[u] = *reinterpret_cast<const uint4*>(h < p.Hk ? krow + (int64_t)h * p.D : vrow + (int64_t)(h - p.Hk) * p.D);
     }
   };
-  load();
+  constexpr int kStep = kGroups * kUnroll;
+  uint4 va[kUnroll], vb[kUnroll];
+  load(va, h0);
+  if (h0 + kStep - g < heads) load(vb, h0 + kStep);
   const bool normed = p.norm_weight != nullptr;
   LaneRope lr;
   lr.on = false;
@@ -295,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
   }
   uint16_t* kdst = p.k_cache + row * p.Hk * p.D + c0;
   uint16_t* vdst = p.v_cache + row * p.Hk * p.D + c0;
-  for (;;) {
+  auto store = [&](const uint4 (&v)[kUnroll], int h0) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int h = h0 + u * kGroups;
@@ -310,22 +323,27 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendParam
       if (live && h < heads)
         *reinterpret_cast<uint4*>(h < p.Hk ? kdst + (int64_t)h * p.D : vdst + (int64_t)(h - p.Hk) * p.D) = o;
     }
-    h0 += kGroups * kUnroll;
+  };
+  for (;;) {
+    store(va, h0);
+    if (h0 + 2 * kStep - g < heads) load(va, h0 + 2 * kStep);
+    h0 += kStep;
     if (h0 - g >= heads) return;
-    load();
+    store(vb, h0);
+    if (h0 + 2 * kStep - g < heads) load(vb, h0 + 2 * kStep);
+    h0 += kStep;
+    if (h0 - g >= heads) return;
   }
 }
 
-// Heads per warp: what its lane groups have in flight at once, fewer when the call
-// is too small to give every SM a few warps that way (a decode step).
+// Heads per warp: a token's, fewer when the call is too small to give every SM a few
+// warps that way (a decode step).
 int head_share(int64_t T, int heads, int lph, int sms) {
   const int groups = 32 / lph;
-  const int64_t warps = 8 * (int64_t)sms;  // wanted
-  int per_group = kUnroll;
-  while (per_group > 1 && T * ((heads + groups * per_group - 1) / (groups * per_group)) < warps) per_group /= 2;
-  const int splits = (heads + groups * per_group - 1) / (groups * per_group);
-  const int share = (heads + splits - 1) / splits;
-  return (share + groups - 1) / groups * groups;  // even shares of whole rounds of the groups
+  const int64_t wanted = (8 * (int64_t)sms + T - 1) / T;  // warps per token
+  const int rounds = (heads + groups - 1) / groups;       // of the lane groups
+  const int splits = (int)(wanted < rounds ? wanted : rounds);
+  return (rounds + splits - 1) / splits * groups;
 }
 
 template <bool BF16, int LPH>
