@@ -376,11 +376,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < cnt; ++i, n += 2) {
           const int key0 = (c->o.j0 + i) * KT;
+          ok = sm100::mbar_wait(&bars.s_full[w], ns++ & 1u, &abort_flag) && ok;
+          ok = __all_sync(0xffffffffu, ok);
           if (key0 < c->o.lo || key0 + KT > c->o.hi) {
             // values behind the sequence's end (or before the window) may hold
-            // anything, a NaN times a weight of 0 included: make them zeros
+            // anything, a NaN times a weight of 0 included: make them zeros. Only now:
+            // these scores say that the ring has come to this tile. A row tile without
+            // rows lets its warps run pieces ahead, and the parity of a stage cannot tell
+            // its phase from the one two rounds before.
             const int st = (n + 1) % C::kStages, klo = c->o.lo, khi = c->o.hi;
-            ok = sm100::mbar_wait(&bars.full[st], (uint32_t)((n + 1) / C::kStages) & 1u, &abort_flag) && ok;
+            ok = __all_sync(0xffffffffu, ok && sm100::mbar_wait(&bars.full[st], (uint32_t)((n + 1) / C::kStages) & 1u, &abort_flag));
             unsigned char* vt = ring + (size_t)st * C::kTileBytes;
             for (int e = r; ok && e < KT * kCols; e += kRows) {
               const int k = e / kCols, ch = e % kCols;
@@ -389,8 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
-          ok = sm100::mbar_wait(&bars.s_full[w], ns++ & 1u, &abort_flag) && ok;
-          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           sm100::tc_fence_after();
           if (warp_rows) {

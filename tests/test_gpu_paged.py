@@ -264,6 +264,20 @@ def test_head_layouts(lib, Hq, Hk):
     attn_case(lib, attn_inputs(Hq, [1, 3], [70, 200], Hq, Hk, 64, 16))
 
 
+@pytest.mark.parametrize("D", [64, 128, 192])
+@pytest.mark.parametrize("window", [0, 500])
+def test_part_filled_items_between_full_ones(lib, D, window):
+    """Items of at most 128 rows (half an item) with long and short contexts between full
+    items: whatever runs ahead in them touches nothing that the others still use."""
+    import torch
+    lens, ctx = [13, 40, 9, 70, 3, 80, 1, 60, 2, 17], [2679, 12, 3000, 1, 1500, 5, 2000, 64, 2500, 0]
+    i = attn_inputs(12, lens * 4, ctx * 4, 14, 2, D, 32)
+    out, lse, args = attn_case(lib, i, window=window)
+    for _ in range(5):
+        o, l = lib.paged_attention(*args, max_len=80, window=window or None, return_lse=True)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
 def test_max_len_unknown_and_padding(lib):
     i = attn_inputs(1, [3, 1, 1], [60, 400, 0], 8, 2, 128, 64, extra_tokens=9)
     a, la, _ = attn_case(lib, i, max_len=None)
