@@ -32,13 +32,16 @@ struct DecodeCfg {
   static constexpr int kM = 8 * NB;
   static constexpr int kTileBytes = kKT * DP * 2;  // K or V
   static constexpr int kStageBytes = 2 * kTileBytes;
-  // Eight consumer warps per SM where their registers allow: two CTAs of four, or
-  // one of eight whose halves (groups) take every other tile.
+  // Eight consumer warps per SM where their registers and the stages allow: two CTAs
+  // of four, or one of eight whose halves (groups) take every other tile. A stage
+  // belongs to one group (an even number of stages): a group that runs ahead would
+  // not know a stage's phase from the one two before by its parity.
   static constexpr int kCtasPerSm = DP <= 128 ? 2 : 1;
-  static constexpr int kGroups = DP > 128 && NB == 1 ? 2 : 1;
+  static constexpr int kGroups = DP == 192 && NB == 1 ? 2 : 1;
   static constexpr int kWarps = 4 * kGroups;  // consumers; warp kWarps produces
   static constexpr int kThreads = (kWarps + 1) * 32;
   static constexpr int kStages = (kCtasPerSm == 2 ? 98304 : 196608) / kStageBytes;
+  static_assert(kStages % kGroups == 0, "a stage belongs to one group");
   static constexpr int kPitch = DP + 4;            // floats per row of a merge buffer
   static constexpr int kMergeBytes = kGroups * kM * kPitch * 4;
   static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + kMergeBytes;

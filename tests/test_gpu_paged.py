@@ -382,3 +382,113 @@ def test_captured_and_replayed(lib):
         eager = step()
         assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
     assert lib.get_error() == 0
+
+
+# ---- together, and at the edges ------------------------------------------------
+
+
+def test_nsa_step_together(lib):
+    """One decode step over both caches of NSA: keys and values appended, the step's windows
+    compressed by nsa_compress, attention over a window of raw rows and over the compressed
+    rows, joined by lse: the softmax over both sets of keys."""
+    import torch
+    block, stride, win, Hq, Hk, D, page = 32, 16, 64, 8, 2, 128, 64
+    ctx = [79, 200, 31, 127, 415]  # new lengths 80, 201, 32, 128, 416: four on a compression step
+    B = len(ctx)
+    i = attn_inputs(21, [1] * B, ctx, Hq, Hk, D, page, rope=64)
+    q, k, v = b16(i.q, "bf16"), b16(i.k, "bf16"), b16(i.v, "bf16")
+    kc, vc = b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16")
+    tbl, cu, sp = dev(i.block_table), dev(i.cu_seqlens), dev(i.start_pos)
+    w, sin, cos = b16(i.weight, "bf16"), dev(i.sin), dev(i.cos)
+    qn, _ = lib.qk_norm_rope(q, None, w, sin=sin, cos=cos)
+    lib.kv_append(k, v, kc, vc, tbl, cu, sp, norm_weight=w, sin=sin, cos=cos)
+    # the compressed rows' cache: sequence b owns block b of 32 rows; rows of earlier steps are there
+    rows = 32
+    g = torch.Generator(device="cuda").manual_seed(3)
+    cmp_k = torch.randn(B, rows, Hk, D, generator=g, device="cuda").bfloat16()
+    cmp_v = torch.randn(B, rows, Hk, D, generator=g, device="cuda").bfloat16()
+    cw = torch.full((block, Hk), 1 / block, device="cuda").bfloat16()
+    lens = [c + 1 for c in ctx]
+    held = [(n - block) // stride + 1 for n in lens]
+    slots = torch.tensor([b * rows + max(h - 1, 0) for b, h in enumerate(held)], dtype=torch.int32, device="cuda")
+    act = torch.tensor(lens, dtype=torch.int64, device="cuda")
+    for src, dst in ((kc, cmp_k), (vc, cmp_v)):
+        before = dst.clone()
+        lib.nsa_compress(src, cw, slots, act, dst.view(B * rows, Hk, D), compress_block_size=block,
+                         compress_stride=stride, block_table=tbl, page_block_size=page)
+        assert not torch.equal(before, dst)
+    ctbl = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    raw = lib.paged_attention(qn, kc, vc, tbl, cu, sp, max_len=1, window=win, return_lse=True)
+    com = lib.paged_attention(qn, cmp_k, cmp_v, ctbl, cu, sp, max_len=1, key_block=block, key_stride=stride,
+                              return_lse=True)
+    assert lib.get_error() == 0
+    f = lambda t: to_f64(bits(t), "bf16")  # noqa: E731
+    ref = [oracle.paged_attention(f(qn), f(a), f(b), t.cpu().numpy(), i.cu_seqlens, i.start_pos, D ** -0.5, **kw)
+           for a, b, t, kw in ((kc, vc, tbl, dict(window=win)),
+                               (cmp_k, cmp_v, ctbl, dict(key_block=block, key_stride=stride)))]
+    for (out, lse), r in zip((raw, com), ref):
+        assert_attention(bits(out), lse.cpu().numpy(), r, "bf16")
+    from tests.paged_helpers import attention_limits
+    total = np.logaddexp(ref[0].lse, ref[1].lse)
+    want = sum(np.exp(r.lse - total)[..., None] * r.out for r in ref)
+    got_total = torch.logaddexp(raw[1].double(), com[1].double())
+    got = sum(torch.exp(x[1].double() - got_total)[..., None] * x[0].double() for x in (raw, com)).cpu().numpy()
+    lim = [attention_limits(r, D, "bf16") for r in ref]
+    # the weights are off by at most the sum of both lse errors, on the difference of the outs
+    tol = np.maximum(lim[0][0], lim[1][0]) + (lim[0][1] + lim[1][1])[..., None] * 2 * (
+        np.abs(ref[0].out) + np.abs(ref[1].out))
+    assert np.all(np.abs(got - want) <= tol)
+
+
+@pytest.mark.parametrize("lens,ctx", [([1, 1, 1], [100, 300, 50]), ([40, 3, 200], [100, 300, 50])])
+def test_nan_reaches_its_own_rows_only(lib, lens, ctx):
+    """A NaN key that every token of sequence 1 sees: its head group's outs and lse there are
+    NaN, all other rows bit for bit what they were."""
+    import torch
+    i = attn_inputs(13, lens, ctx, 8, 2, 128, 64)
+    out, lse, args = attn_case(lib, i)
+    kc = args[1].clone()
+    kc[int(i.block_table[1][0]), 7, 1] = float("nan")
+    o, l = lib.paged_attention(args[0], kc, *args[2:], max_len=max(lens), return_lse=True)
+    assert lib.get_error() == 0
+    t0, t1 = int(i.cu_seqlens[1]), int(i.cu_seqlens[2])
+    hit = torch.zeros_like(l, dtype=torch.bool)
+    hit[t0:t1, 4:] = True
+    assert torch.isnan(l[hit]).all() and torch.isnan(o[hit]).all()
+    assert torch.equal(l[~hit], lse[~hit]) and torch.equal(o[~hit], out[~hit])
+
+
+def test_only_padding(lib):
+    import torch
+    i = attn_inputs(14, [0, 0], [30, 40], 8, 2, 64, 16, extra_tokens=5)
+    attn_case(lib, i, max_len=5)
+    attn_case(lib, i, max_len=1)
+    append_case(lib, i)
+    torch.cuda.synchronize()
+
+
+def test_caches_past_2_31_elements(lib):
+    """Blocks at the far end of caches of 4.6e9 elements each."""
+    import torch
+    blocks, page, Hk, D = 70000, 64, 8, 128
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24 << 30:
+        pytest.skip("needs 24 GB of free device memory")
+    i = attn_inputs(15, [1, 33], [130, 100], 16, Hk, D, page)
+    n = i.k_cache.shape[0]
+    kc, vc = (torch.empty((blocks, page, Hk, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kc[blocks - n:], vc[blocks - n:] = b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16")
+    tbl = dev(np.where(i.block_table >= 0, i.block_table + blocks - n, -1).astype(np.int32))
+    cu, sp = dev(i.cu_seqlens), dev(i.start_pos)
+    small_k, small_v, small_tbl = b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16"), dev(i.block_table)
+    k, v, q = b16(i.k, "bf16"), b16(i.v, "bf16"), b16(i.q, "bf16")
+    lib.kv_append(k, v, kc, vc, tbl, cu, sp)
+    lib.kv_append(k, v, small_k, small_v, small_tbl, cu, sp)
+    assert torch.equal(kc[blocks - n:], small_k) and torch.equal(vc[blocks - n:], small_v)
+    for sel, ml in ((slice(0, 1), 1), (slice(0, 34), 33)):
+        c = cu[:2] if ml == 1 else cu
+        a = lib.paged_attention(q[sel], kc, vc, tbl[:len(c) - 1], c, sp[:len(c) - 1], max_len=ml, return_lse=True)
+        b = lib.paged_attention(q[sel], small_k, small_v, small_tbl[:len(c) - 1], c, sp[:len(c) - 1], max_len=ml,
+                                return_lse=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert lib.get_error() == 0
