@@ -395,8 +395,8 @@ typedef struct cmp_attn_dims {
  *   workspace    device, workspace_bytes >= cmp_paged_attention_workspace(dims), 16-byte
  *                aligned; its contents need no preparation and mean nothing afterwards.
  *                Calls that may overlap need one each.
- * A sequence longer than max_len, or whose cu_seqlens or start_pos entries are not
- * usable, is skipped and reported (its rows are left as they were); a missing
+ * A sequence longer than max_len, whose cu_seqlens or start_pos entries are not
+ * usable, or with positions past INT32_MAX - 1024 is skipped and reported (its rows are left as they were); a missing
  * table entry reads as zeros and is reported. Results do not depend on timing
  * (no floating-point atomics).
  * Returns CMP_OK, CMP_ERR_NULLPTR, CMP_ERR_INVALID, CMP_ERR_UNSUPPORTED (dtype) or
@@ -407,7 +407,8 @@ CMP_API int cmp_paged_attention(const void* q, const void* k_cache, const void* 
                                 void* workspace, size_t workspace_bytes, void* stream, const cmp_attn_dims* dims);
 
 /* Bytes of workspace such a call needs on the current device (0: invalid dims).
- * Depends on D, Hq / Hk and max_len (or T) only. Host only. */
+ * Depends on D and on whether a sequence has at most 8, at most 16 or more rows per
+ * key head (max_len, or T, times Hq / Hk). Host only. */
 CMP_API size_t cmp_paged_attention_workspace(const cmp_attn_dims* dims);
 
 /* ---- measurement --------------------------------------------------------
@@ -427,7 +428,7 @@ enum {
   CMP_KERNEL_NSA_SCAN = 10,    /* NsaCompressWithCache, packed layout: each batch's first row */
   CMP_KERNEL_QK_NORM_ROPE = 11,
   CMP_KERNEL_KV_APPEND = 12,
-  CMP_KERNEL_ATTN_DECODE = 13,  /* paged attention, few rows per key head */
+  CMP_KERNEL_ATTN_DECODE = 13,  /* paged attention, at most 16 rows per key head and sequence */
   CMP_KERNEL_ATTN_COMBINE = 14, /* paged attention: joins rows that were cut between CTAs */
   CMP_KERNEL_ATTN_CHUNK = 15,   /* paged attention, many rows per key head */
   CMP_KERNEL_COUNT = 16

