@@ -277,15 +277,24 @@ _torch = None
 _DTYPE = {}  # torch dtype -> CMP_NSA_FP16 / CMP_NSA_BF16
 
 
-# The paged operators' calls are short (a decode step's append takes 3 us on the device), so
-# their checks look at each tensor once, without torch.device objects and without entering a
-# device context when the tensors are on the current device; what fails a check is described by
-# _check and _check_tokens.
+_calls = None  # binding/fast.cpp; None with another library than the one it links
+
+
+# The paged operators' calls are short (a decode step's append takes 5 us on the device), so
+# the usual ones go through _calls: tensors on the current device, on its current stream. It
+# returns -1, having done nothing, for every other call; the code below it then handles that
+# or says what is wrong.
 
 def _torch_module():
-    global _torch
+    global _torch, _calls
     if _torch is None:
         import torch
+        if not os.environ.get("CMP_LIBRARY"):
+            if not os.path.exists(os.path.join(_PKG, "_fast.so")):
+                raise ImportError("_fast.so is missing: build it with "
+                                  "`python -c 'import __graft_entry__ as g; g.build()'`")
+            from . import _fast
+            _calls = _fast
         _DTYPE.update({torch.float16: 0, torch.bfloat16: 1})
         _torch = torch
     return _torch
@@ -378,7 +387,13 @@ def qk_norm_rope(q, k, q_weight, k_weight=None, *, sin=None, cos=None, rope_pair
     channels of a head are rotated; None: no rotation), ``rope_pairs`` "interleaved"
     (channels 2j, 2j+1) or "halves" (j, dim/2 + j). ``q_out`` / ``k_out`` may be q / k
     (in place); new dense tensors by default."""
-    torch = _torch_module()
+    torch = _torch or _torch_module()
+    if stream is None and _calls is not None:
+        r = _calls.qk_norm_rope(q, k, q_weight, k_weight, sin, cos, rope_pairs, eps, q_out, k_out)
+        if r.__class__ is tuple:
+            return r
+        if r > 0:
+            raise CmpError(r, "cmp_qk_norm_rope")
     dt = _dtype16(q, "q", torch)
     dev, idx, dtype = q.device, q.get_device(), q.dtype
     if q.dim() != 3:
@@ -451,7 +466,14 @@ def kv_append(k, v, k_cache, v_cache, block_table, cu_seqlens, start_pos=None, *
     k, v [T, Hk, D] fp16 / bf16, last two dimensions dense; caches [block_num, page_size,
     Hk, D]; block_table int32 [B, pages]; cu_seqlens int32 [B+1]; start_pos int32 [B] or
     None; norm_weight [D]; sin / cos [T, dim] float32 or bf16, as for ``qk_norm_rope``."""
-    torch = _torch_module()
+    torch = _torch or _torch_module()
+    if stream is None and _calls is not None:
+        r = _calls.kv_append(k, v, k_cache, v_cache, block_table, cu_seqlens, start_pos, norm_weight, sin, cos,
+                            rope_pairs, eps)
+        if r == CMP_OK:
+            return k_cache, v_cache
+        if r > 0:
+            raise CmpError(r, "cmp_kv_append")
     dt = _dtype16(k, "k", torch)
     dev, idx, dtype = k.device, k.get_device(), k.dtype
     if k.dim() != 3:
@@ -490,7 +512,14 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos=None
     keys a token sees at most; ``key_block`` / ``key_stride`` describe caches of compressed
     rows. ``workspace``: a CUDA tensor of at least ``paged_attention_workspace`` bytes
     (allocated per call by default)."""
-    torch = _torch_module()
+    torch = _torch or _torch_module()
+    if stream is None and _calls is not None:
+        r = _calls.paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos, scale, max_len, window,
+                                  key_block, key_stride, out, lse, return_lse, workspace)
+        if r.__class__ is not int:
+            return r
+        if r > 0:
+            raise CmpError(r, "cmp_paged_attention")
     dt = _dtype16(q, "q", torch)
     dev, idx, dtype = q.device, q.get_device(), q.dtype
     if q.dim() != 3:

@@ -1,5 +1,8 @@
 """Build the CUDA library in-tree with nvcc for sm_100a.
 
+It also compiles binding/fast.cpp with g++ against PyTorch's headers into _fast.so
+(the paged operators' calls without the interpreter), which links the library.
+
 The shared library statically links the CUDA runtime and exports only the
 ``cmp_*`` entry points declared in include/cmp.h, so it can be loaded next to
 any other CUDA runtime (for example PyTorch's) without symbol clashes.
@@ -9,9 +12,11 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libcmp_b200.so")
+FAST_SRC = os.path.join(PKG, "binding", "fast.cpp")
+FAST = os.path.join(PKG, "_fast.so")
 # measurement build: the same sources with the decode kernel's phase stamps
 # (-DCMP_PHASE_STAMPS), for bench.py --only decode-phases
 PHASES_OBJDIR = os.path.join(PKG, "_build", "phases")
@@ -78,7 +85,31 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False,
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    if not phases:
+        build_fast(verbose, force)
     return lib
+
+
+def build_fast(verbose: bool = False, force: bool = False) -> str:
+    """Compile binding/fast.cpp against PyTorch's headers. Returns the module's path."""
+    newest = max(os.path.getmtime(f) for f in [FAST_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if not force and os.path.exists(FAST) and os.path.getmtime(FAST) >= newest:
+        return FAST
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]  # without importing it
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    libs = os.path.join(torch, "lib")
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"],
+           FAST_SRC, "-o", FAST, "-L", libs, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-L", PKG, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + libs]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for fast.cpp:\n{r.stdout}\n{r.stderr}")
+    return FAST
 
 
 if __name__ == "__main__":
