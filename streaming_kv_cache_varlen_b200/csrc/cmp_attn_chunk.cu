@@ -21,8 +21,8 @@
 // Bound by the chain scores - softmax - weights - products of a row tile, of which two
 // run in turn: 128 keys of a pair of tiles take 3400 clocks, of which the tensor core
 // works 2050 and the special function unit 2050 (16 exponentials a clock). 4096 tokens
-// of 32 heads of 128 over 16384 positions (962 GFLOP) take 746 us, 0.79 of the measured
-// matrix product burst. Measured and not kept: 2^x by polynomial for 1/8 to 3/8 of the
+// of 32 heads of 128 over 16384 positions (962 GFLOP) take 715 us, 0.82 of the measured
+// matrix product burst (845 us back to back, where power limits the clock). Measured and not kept: 2^x by polynomial for 1/8 to 3/8 of the
 // weights (as fast or slower: its 15 instructions a pair take the issue slots that the
 // special function unit leaves), half a row per thread on 16 softmax warps (800 us: a
 // second pass over TMEM, as 64 scores and the rest do not fit 104 registers), tiles of
