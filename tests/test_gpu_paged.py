@@ -290,6 +290,17 @@ def test_max_len_unknown_and_padding(lib):
     attn_case(lib, i, max_len=3)
 
 
+@pytest.mark.parametrize("max_len", [2, 20])
+def test_many_sequences(lib, max_len):
+    """1200 sequences (several per thread of a CTA's plan), a third of them without tokens,
+    as decoding (four rows per key head) and as chunks (20 tokens may come)."""
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(0, 3, 1200)]
+    if max_len > 2:
+        lens[700] = 20
+    attn_case(lib, attn_inputs(16, lens, [int(x) for x in rng.integers(0, 90, 1200)], 4, 2, 64, 16), max_len=max_len)
+
+
 def test_strided_queries(lib):
     import torch
     i = attn_inputs(2, [40, 1], [100, 500], 8, 2, 128, 64)
