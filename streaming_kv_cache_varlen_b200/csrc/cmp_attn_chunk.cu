@@ -406,6 +406,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(vt + (ch >> 3) * (KT * 128) + k * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            // lane 0 arrives for the warp; a warp without rows does so with nothing else between
+            __syncwarp();
           }
           if (!ok) break;
           sm100::tc_fence_after();

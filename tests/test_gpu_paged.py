@@ -265,6 +265,15 @@ def test_unseen_rows_may_hold_anything(lib, stale, dtype, lens, ctx, window, D):
     attn_case(lib, attn_inputs(9, lens, ctx, 8, 2, D, 64, dtype), window=window, stale=stale)
 
 
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("rows", [1, 32, 33, 64, 96, 160, 224])
+def test_warps_without_rows_clear_stale_values(lib, D, rows):
+    """Items whose last row tile leaves one to three of its warps without rows: their lanes
+    clear a part of the last key tile's values too, before the product reads any of them."""
+    lens, ctx = [rows, 256 + rows, rows, 17], [3, 700, 1999, 90]
+    attn_case(lib, attn_inputs(rows + D, lens, ctx, 2, 2, D, 32), stale=float("nan"), max_len=max(lens))
+
+
 @pytest.mark.parametrize("Hq,Hk", [(128, 1), (16, 1), (17, 1), (64, 64), (15, 5), (36, 12)])
 def test_head_layouts(lib, Hq, Hk):
     attn_case(lib, attn_inputs(Hq, [1, 3], [70, 200], Hq, Hk, 64, 16))
