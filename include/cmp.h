@@ -483,8 +483,11 @@ CMP_API int cmp_set_proj_kernel(int which);
  * bounded wait gives up after about one second, the rows of the call come out
  * as zeros, the CTAs free their tensor memory and return, and cmp_get_error
  * then reports CMP_ERR_TIMEOUT and resets the exchange words, so the next call
- * runs normally. Nothing faults or hangs. Returns the previous count, or -1 if
- * launches < 0. */
+ * runs normally. A cmp_paged_attention call that decodes counts as such a launch
+ * too: no key tile is loaded for it, its CTAs' waits give up after two seconds,
+ * its rows come out as zeros (those that span several CTAs too, lse -inf) and
+ * cmp_get_error reports CMP_ERR_TIMEOUT. Nothing faults or hangs. Returns the
+ * previous count, or -1 if launches < 0. */
 CMP_API int cmp_debug_unreachable_barrier(int launches);
 
 #ifdef __cplusplus

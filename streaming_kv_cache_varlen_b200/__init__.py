@@ -665,7 +665,8 @@ def profile_stop() -> Dict[str, Tuple[float, int]]:
 def debug_unreachable_barrier(launches: int) -> int:
     """Testing knob: the next ``launches`` channel-group decode launches time out
     at their grid barrier (about 1 s each; get_error then reports
-    CMP_ERR_TIMEOUT). Returns the previous count."""
+    CMP_ERR_TIMEOUT), or as many decoding calls of ``paged_attention`` at their
+    first key tile (about 2 s each). Returns the previous count."""
     return int(lib.cmp_debug_unreachable_barrier(launches))
 
 

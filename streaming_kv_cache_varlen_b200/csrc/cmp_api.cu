@@ -142,7 +142,15 @@ std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 std::map<std::pair<int, cudaStream_t>, unsigned> g_pending_err;  // kept across a regrow
 std::atomic<int64_t> g_launches{0};
 std::atomic<int> g_proj_kernel{0};
-std::atomic<int> g_unreachable_barrier{0};  // launches left whose grid barrier cannot be reached
+std::atomic<int> g_unreachable_barrier{0};  // launches left whose waits cannot be met
+
+// The timeout tests' knob, consumed one launch at a time.
+bool take_unreachable() {
+  bool taken = false;
+  for (int v = g_unreachable_barrier.load(); v > 0 && !taken;)
+    taken = g_unreachable_barrier.compare_exchange_weak(v, v - 1);
+  return taken;
+}
 
 // ---- profiling ---------------------------------------------------------------
 
@@ -349,9 +357,7 @@ int run_path(Params& p, int which, cudaStream_t s) {
     void* counter = ws + L.err + kCounterOffset;
     void* xch = ws + L.err + kExchangeOffset;
     void* urow = ws + L.err + kRotateOffset;
-    bool unreachable = false;  // the timeout test's knob, consumed one launch at a time
-    for (int v = g_unreachable_barrier.load(); v > 0 && !unreachable;)
-      unreachable = g_unreachable_barrier.compare_exchange_weak(v, v - 1);
+    const bool unreachable = take_unreachable();
     const cudaError_t e = launch(CMP_KERNEL_DECODE_CP, s,
                                  [&] { return cmp::launch_decode_cp(p, counter, xch, urow, s, unreachable); });
     if (e == cudaErrorNotSupported) return kRetryOtherPath;
@@ -731,6 +737,7 @@ int cmp_paged_attention(const void* q, const void* k_cache, const void* v_cache,
   p.key_stride = (int)key_stride;
   p.window = (int)window;
   p.max_len = (int)(d.max_len && d.max_len < d.T ? d.max_len : d.T);
+  p.withhold = !a.chunk && take_unreachable() ? 1 : 0;
   p.run_shift = 4;
   while ((1 << p.run_shift) < a.key_tile && p.page % (2 << p.run_shift) == 0) ++p.run_shift;
   p.div_g = cmp::make_fast_div(p.G);

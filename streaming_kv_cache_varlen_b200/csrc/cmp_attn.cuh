@@ -43,6 +43,7 @@ struct AttnParams {
   FastDiv div_g, div_stride, div_page;  // by G, key_stride, page
   int key_block, key_stride, window;    // window 0: none
   int max_len;
+  int withhold;       // testing: no tile is loaded, every wait for one runs out (decoding)
   int run_shift;      // keys per TMA box: 1 << run_shift, a divisor of the page
   float scale_log2;   // scale * log2(e)
 };

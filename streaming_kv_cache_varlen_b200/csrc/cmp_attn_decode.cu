@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP, NB>::kThreads, DecodeCfg<DP, NB>
     uint32_t par = 0;
     bool alive = true;
     AttnPiece o;
-    while (alive && walk.next(o)) {
+    while (alive && !p.withhold && walk.next(o)) {
       if (o.hi <= o.lo) continue;
       const int32_t* trow = p.table + (int64_t)o.b * p.table_stride;
       for (int j = o.j0; j < o.j1; ++j, ++n) {
@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP, NB>::kThreads, DecodeCfg<DP, NB>
   uint32_t par = 0;
   AttnPiece o;
   bool begun = false;
+  bool ok = true;  // no wait of this warp has given up; the same in all its lanes
   if (start.units == 0 && tid == 0) attn_write_desc(p, blockIdx.x, 0, nullptr);
   while (walk.next(o)) {
     // Q^T fragments (row 8 nb + g, channels 2 t4, + 1 and + 8, + 9 of a step), zeros
@@ -191,14 +192,14 @@ __global__ void __launch_bounds__(DecodeCfg<DP, NB>::kThreads, DecodeCfg<DP, NB>
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int r = 8 * b + g;
-      const bool ok = r < o.rows;
-      const int rr = o.row0 + (ok ? r : 0);
+      const bool there = r < o.rows;
+      const int rr = o.row0 + (there ? r : 0);
       const int tok = p.div_g.div(rr);
       const uint16_t* src = p.q + (int64_t)(o.s.t0 + tok) * p.q_stride + (int64_t)(o.h * p.G + rr - tok * p.G) * p.D;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int c = k * 16 + 2 * t4;
-        const bool in = ok && k * 16 < p.D;
+        const bool in = there && k * 16 < p.D;
         qf[k][b][0] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + c)) : 0u;
         qf[k][b][1] = in ? __ldg(reinterpret_cast<const uint32_t*>(src + c + 8)) : 0u;
       }
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP, NB>::kThreads, DecodeCfg<DP, NB>
     if (o.hi > o.lo) {
       for (int j = o.j0; j < o.j1; ++j, ++n) {
         if ((n & (kGroups - 1)) == group) {
-          const bool ok = sm100::mbar_wait(&full[st], par, &abort_flag);
+          ok = __all_sync(0xffffffffu, ok && sm100::mbar_wait(&full[st], par, &abort_flag));
           unsigned char* kt = ring + (size_t)st * C::kStageBytes;
           unsigned char* vt = kt + C::kTileBytes;
           const int key0 = j * kKT + quarter * 16;  // this warp's keys
@@ -417,6 +418,7 @@ __global__ void __launch_bounds__(DecodeCfg<DP, NB>::kThreads, DecodeCfg<DP, NB>
     }
     bar_consumers<kWarps>();  // wm, wl and merge are free again
   }
+  if (!ok && lane == 0) atomicOr(&g_attn_err, kErrTimeout);
   if (tid == 0 && !begun && start.units > 0) attn_write_desc(p, blockIdx.x, 0, nullptr);
 }
 

@@ -387,6 +387,26 @@ def test_bad_entries_are_reported(lib):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("D,heads,tokens", [(128, (8, 2), 1), (192, (8, 4), 1), (256, (4, 1), 3)])
+def test_waits_that_give_up_are_reported(lib, D, heads, tokens):
+    """A decoding call whose key tiles never come: every warp gives up as one, the call ends,
+    says so once, and the next call is right again."""
+    import torch
+    i = attn_inputs(D, [tokens] * 3, [100, 700, 3000], *heads, D, 64)
+    out, lse, args = attn_case(lib, i)
+    try:
+        assert lib.debug_unreachable_barrier(1) == 0
+        o, l = lib.paged_attention(*args, max_len=tokens, return_lse=True)
+        torch.cuda.synchronize()
+        assert lib.debug_unreachable_barrier(0) == 0                  # the knob was consumed
+    finally:
+        lib.debug_unreachable_barrier(0)
+    assert lib.get_error() == 6 and lib.get_error() == 0
+    assert torch.all(o == 0) and torch.all(torch.isneginf(l))
+    again, lse2 = lib.paged_attention(*args, max_len=tokens, return_lse=True)
+    assert lib.get_error() == 0 and torch.equal(again, out) and torch.equal(lse2, lse)
+
+
 def test_captured_and_replayed(lib):
     """A decode step of all three operators in a graph, replayed after its inputs moved on."""
     import torch
