@@ -366,7 +366,8 @@ def _handle(stream, idx, torch):
 
 def _on_stream(handle, dev, torch):
     """Context in which tensors are allocated that belong to the stream `handle`."""
-    return torch.cuda.stream(torch.cuda.ExternalStream(handle, dev))
+    # ExternalStream(0) is a new stream, not the default one
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, dev) if handle else torch.cuda.default_stream(dev))
 
 
 def _on_device(idx, torch, call, *args):

@@ -387,6 +387,30 @@ def test_bad_entries_are_reported(lib):
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_default_stream_by_name(lib, raw):
+    """The default stream given explicitly (its handle is 0) while another one is current: the
+    call runs there, and what it allocates belongs to it."""
+    import torch
+    d = torch.device("cuda", torch.cuda.current_device())
+    default = torch.cuda.default_stream()
+    i = attn_inputs(33, [1, 30], [70, 200], 8, 2, 64, 16, rope=32)
+    args = [b16(i.q, "bf16"), b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16"), dev(i.block_table), dev(i.cu_seqlens),
+            dev(i.start_pos)]
+    w = b16(i.weight, "bf16")
+    want = lib.paged_attention(*args, max_len=30)
+    want_q, _ = lib.qk_norm_rope(args[0], None, w)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with lib._on_stream(0, d, torch):
+            assert torch.cuda.current_stream() == default
+        s = 0 if raw else default
+        assert torch.equal(lib.paged_attention(*args, max_len=30, stream=s), want)
+        assert torch.equal(lib.qk_norm_rope(args[0], None, w, stream=s)[0], want_q)
+    torch.cuda.synchronize()
+    assert lib.get_error() == 0
+
+
 @pytest.mark.parametrize("D,heads,tokens", [(128, (8, 2), 1), (192, (8, 4), 1), (256, (4, 1), 3)])
 def test_waits_that_give_up_are_reported(lib, D, heads, tokens):
     """A decoding call whose key tiles never come: every warp gives up as one, the call ends,
