@@ -16,8 +16,8 @@
 // a share of one token's heads, kUnroll heads per lane group with all their loads
 // in flight, and keeps the token's table values (16-byte loads) and the weights in
 // registers, two batches in turn; for kv_append it looks up its token's cache row meanwhile, so a CTA
-// needs no barrier. 16384 tokens of 40 heads of 128, fully rotated, take 80 us (352 MB:
-// 0.67 of the measured copy rate; one CTA per token with four-byte table loads took
+// needs no barrier. 16384 tokens of 40 heads of 128, fully rotated, take 82 us (352 MB:
+// 0.65 of the measured copy rate; one CTA per token with four-byte table loads took
 // 112), the keys and values of 23000 tokens of 8 heads 47 us (214 MB, 0.69; 92).
 #include "cmp_internal.cuh"
 
@@ -132,6 +132,24 @@ __device__ __forceinline__ void load_rope(const RopeTable& r, int64_t token, int
   }
 }
 
+// Sum over the LPH lanes of a head, in all of them.
+template <int LPH>
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+  for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o, LPH);
+  return v;
+}
+
+// Mean squares (plus eps) between which no square of weight has left fp32's range.
+// Beyond, a head of bf16 values is scaled by a power of two, which is exact and cancels.
+// Above: some channel is 2^60 or more, so with 2^-70 the largest square lies in
+// 2^-20 .. 2^116. Below (only with an eps below 1e-30): every channel is under 2^-46, so
+// with 2^80 the squares lie in 2^-106 (bf16's smallest number) .. 2^68. Asking costs 3 %
+// (16384 tokens of 40 heads of 128: 82.3 us, 79.9 without); asking once for two or four
+// heads, which all have to be kept for it, takes 86 and 84.6.
+constexpr float kMeanSquareMin = 1e-30f, kMeanSquareMax = 3.4028234e38f;
+constexpr float kScaleDown = 0x1p-70f, kScaleUp = 0x1p80f;
+
 // One head's 8 channels per lane: norm (with the weights wv, if normed) and
 // rotation. Every lane of the warp takes part; lanes past D hold zeros.
 template <bool BF16, int LPH>
@@ -141,9 +159,19 @@ __device__ __forceinline__ void norm_rope(float (&x)[8], bool normed, const uint
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    const float ms = fmaf(head_sum<LPH>(ss), inv_d, eps);
+    float sc = rsqrtf(ms);
+    // fp16's squares stay in range (2^-48 to 2^32)
+    if (BF16 && __any_sync(0xffffffffu, !(ms >= kMeanSquareMin && ms <= kMeanSquareMax))) {
+      const float f = ms > kMeanSquareMax ? kScaleDown : ms < kMeanSquareMin ? kScaleUp : 1.f;
+      ss = 0.f;
 #pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o, LPH);
-    const float sc = rsqrtf(fmaf(ss, inv_d, eps));
+      for (int e = 0; e < 8; ++e) {
+        x[e] *= f;
+        ss = fmaf(x[e], x[e], ss);
+      }
+      sc = rsqrtf(fmaf(head_sum<LPH>(ss), inv_d, eps * f * f));
+    }
     float w[8];
     unpack8<BF16>(wv, w);
 #pragma unroll

@@ -73,6 +73,52 @@ def test_norm_queries_only_and_zero_rows(lib):
     assert out.shape == (0, 2, 64)
 
 
+@pytest.mark.parametrize("D", [16, 64, 80, 128, 192, 256])
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+def test_norm_over_the_whole_range(lib, D, eps):
+    """Heads whose squares leave the range of fp32: up to bf16's largest value, and with eps = 0
+    down to its smallest ones; ordinary heads beside them are what they are without them."""
+    import torch
+    from workloads.synth import bf16_bits
+    mags = np.float32([1.0, 3.3e38, 1e30, 2e19, 1.7e19, 1e18, 1e-3] + ([1e-19, 1e-25, 1e-38] if eps == 0 else [1e-3]))
+    rng = np.random.default_rng(D)
+    x = rng.uniform(-1, 1, (9, len(mags), D)).astype(np.float32)
+    x[..., 0] = 1.0
+    xb = bf16_bits(x * mags[None, :, None])
+    i = make_paged_inputs(seed=D, lens=[9], ctx=[3], Hq=1, Hk=1, D=D, page=16, rope=16)
+    w, sin, cos = b16(i.weight, "bf16"), dev(i.sin), dev(i.cos)
+    q = b16(xb, "bf16")
+    out, none = lib.qk_norm_rope(q, None, w, sin=sin, cos=cos, eps=eps)
+    ref, mag = oracle.norm_rope(to_f64(xb, "bf16"), to_f64(i.weight, "bf16"), i.sin, i.cos, "interleaved", eps)
+    assert_normed(bits(out), ref, mag, "bf16")
+    one, none = lib.qk_norm_rope(q[:, :1], None, w, sin=sin, cos=cos, eps=eps)
+    assert torch.equal(one, out[:, :1])
+    # the same keys appended
+    H = len(mags)
+    kc, vc = (torch.zeros(1, 16, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lib.kv_append(q, q, kc, vc, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), dev(i.cu_seqlens), None,
+                  norm_weight=w, sin=sin, cos=cos, eps=eps)
+    assert lib.get_error() == 0
+    assert torch.equal(kc[0, :9], out) and torch.equal(vc[0, :9], q)
+
+
+def test_norm_of_infinities_and_zeros(lib):
+    """As the formula has it: beside an infinity finite channels are 0 and the infinity is NaN; a
+    NaN makes its head NaN; a head of zeros is 0, and NaN (0 / 0) without eps. Other heads stay."""
+    import torch
+    x = torch.ones(4, 3, 64, dtype=torch.bfloat16, device="cuda")
+    x[1, 1, 5] = float("inf")
+    x[2, 1, 5] = float("nan")
+    x[3, 1] = 0
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    for eps in (0.0, 1e-6):
+        y, _ = lib.qk_norm_rope(x, None, w, eps=eps)
+        assert torch.all(y[:, ::2] == 1) and torch.all(y[0, 1] == 1)
+        assert torch.isnan(y[1, 1, 5]) and torch.all(y[1, 1, :5] == 0) and torch.all(y[1, 1, 6:] == 0)
+        assert torch.isnan(y[2, 1]).all()
+        assert torch.isnan(y[3, 1]).all() if eps == 0 else torch.all(y[3, 1] == 0)
+
+
 # ---- kv_append ---------------------------------------------------------------
 
 
