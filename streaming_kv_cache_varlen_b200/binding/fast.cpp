@@ -222,7 +222,12 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   d.block_num = kc->size(0);
   d.page_size = kc->size(1);
   d.table_stride = table->size(1);
-  const bool want_lse = a[12] != Py_None || a[13] == Py_True;
+  const int asked = PyObject_IsTrue(a[13]);  // any truth value, as in the Python path
+  if (asked < 0) {
+    PyErr_Clear();
+    return status(-1);
+  }
+  const bool want_lse = a[12] != Py_None || asked;
   Tensor out_new, lse_new, ws_new;
   if (a[11] != Py_None &&
       (!c.dense(out, c.dtype, 3) || out->size(0) != d.T || out->size(1) != d.Hq || out->size(2) != d.D))

@@ -457,6 +457,91 @@ def test_default_stream_by_name(lib, raw):
     assert lib.get_error() == 0
 
 
+@pytest.mark.parametrize("flag", [True, 1, np.True_, False, 0, np.False_, None])
+def test_return_lse_is_a_truth_value(lib, flag):
+    """The compiled binding (no stream given) and the Python one (a stream) take the same flags."""
+    import torch
+    i = attn_inputs(31, [1, 1], [70, 200], 8, 2, 64, 16)
+    args = [b16(i.q, "bf16"), b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16"), dev(i.block_table), dev(i.cu_seqlens),
+            dev(i.start_pos)]
+    for stream in (None, torch.cuda.current_stream()):
+        r = lib.paged_attention(*args, max_len=1, return_lse=flag, stream=stream)
+        assert type(r) is (tuple if flag else torch.Tensor)
+    assert lib.get_error() == 0
+
+
+def test_both_bindings_agree(lib, monkeypatch):
+    """The compiled binding against the Python one: the same results, or the same refusals."""
+    import torch
+    i = attn_inputs(32, [2, 1], [70, 200], 8, 2, 64, 16, rope=32)
+    q, k, v = (b16(a, "bf16") for a in (i.q, i.k, i.v))
+    kc, vc, tbl, cu, sp = (b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16"), dev(i.block_table), dev(i.cu_seqlens),
+                           dev(i.start_pos))
+    w, sin, cos = b16(i.weight, "bf16"), dev(i.sin), dev(i.cos)
+    out, lse = torch.empty_like(q), torch.empty(3, 8, device="cuda")
+    odd = torch.empty(3 * 8 * 64 + 1, dtype=q.dtype, device="cuda")[1:].view(3, 8, 64)
+    ws = torch.empty(lib.paged_attention_workspace(3, 8, 2, 64, 2), dtype=torch.uint8, device="cuda")
+
+    def norm(*a, **kw):
+        return lib.qk_norm_rope(*a, **kw)
+
+    def append(*a, **kw):
+        return lib.kv_append(*a[:2], kc.clone(), vc.clone(), *a[2:], **kw)
+
+    def attn(*a, **kw):
+        return lib.paged_attention(*a, **{"max_len": 2, **kw})
+
+    A, N, P = (q, kc, vc, tbl, cu, sp), (q, k, w, w), (k, v, tbl, cu, sp)
+    calls = [(norm, N, {}), (norm, N, dict(sin=sin, cos=cos, rope_pairs="halves", eps=0)), (norm, (q, None, w), {}),
+             (norm, N, dict(sin=sin)), (norm, N, dict(sin=sin, cos=cos[:, :16])), (norm, N, dict(rope_pairs="x")),
+             (norm, N, dict(eps=-1.0)), (norm, N, dict(eps=float("nan"))), (norm, N, dict(eps="1")),
+             (norm, N, dict(eps=10 ** 400)), (norm, N, dict(eps=np.float32(1e-5))), (norm, (q, k, w), {}),
+             (norm, (q, k, w, w[:32]), {}), (norm, (q, k[:2], w, w), {}), (norm, (q.float(), k, w, w), {}),
+             (norm, (q, k.half(), w, w), {}), (norm, N, dict(q_out=odd)), (norm, N, dict(q_out=out[:, :, :32])),
+             (norm, (q.cpu(), k, w, w), {}), (norm, (q, k.cpu(), w, w), {}), (norm, (None, k, w, w), {}),
+             (norm, (q[:0], k[:0], w, w), {}), (norm, (q.transpose(1, 2), k, w, w), {}), (norm, (q[:, :, ::2], None, w), {}),
+             (append, P, {}), (append, P, dict(norm_weight=w, sin=sin, cos=cos)), (append, P[:4], {}),
+             (append, P, dict(norm_weight=w.float())), (append, P, dict(sin=sin.half(), cos=cos.half())),
+             (append, (k, v[:, :1], tbl, cu, sp), {}), (append, (k, None, tbl, cu, sp), {}),
+             (append, (k, v, tbl.long(), cu, sp), {}), (append, (k, v, tbl[:1], cu, sp), {}),
+             (append, (k, v, tbl.t(), cu, sp), {}), (append, (k, v, tbl, cu[:0], sp), {}),
+             (append, (k, v, tbl, cu, sp[:1]), {}), (append, P, dict(eps=float("inf"))), (append, P, dict(rope_pairs=None)),
+             (attn, A, {}), (attn, A, dict(return_lse=True)), (attn, A, dict(lse=lse)), (attn, A, dict(out=out)),
+             (attn, A, dict(out=out, lse=lse, workspace=ws)), (attn, A, dict(workspace=ws[:-1])),
+             (attn, A, dict(workspace=ws.cpu())), (attn, A, dict(out=odd)), (attn, A, dict(out=out[:2])),
+             (attn, A, dict(lse=lse.double())), (attn, A, dict(max_len=0)), (attn, A, dict(max_len=None)),
+             (attn, A, dict(max_len=2.0)), (attn, A, dict(max_len=np.int64(2))), (attn, A, dict(max_len=True)),
+             (attn, A, dict(max_len=2 ** 31)), (attn, A, dict(window=0)), (attn, A, dict(window=-1)),
+             (attn, A, dict(window=7)), (attn, A, dict(window=2 ** 31)), (attn, A, dict(window=1.5)),
+             (attn, A, dict(key_block=0)), (attn, A, dict(key_block=None)), (attn, A, dict(key_stride=-2)),
+             (attn, A, dict(key_block=4, key_stride=4, return_lse=True)), (attn, A, dict(scale=0)), (attn, A, dict(scale=1)),
+             (attn, A, dict(scale=np.float64(0.25))), (attn, A, dict(scale=float("nan"))), (attn, A, dict(scale=1e300)),
+             (attn, A, dict(scale="1")), (attn, A[:5], {}), (attn, (q[:, :7], *A[1:]), {}), (attn, (q, kc.half(), *A[2:]), {}),
+             (attn, (q, kc, vc[:1], *A[3:]), {}), (attn, (q, kc[:, :8], vc[:, :8], *A[3:]), {}), (attn, (q[:0], *A[1:]), {}),
+             (attn, (q, kc, vc, tbl[:0], cu[:1], sp[:0]), {}), (attn, (q[:0], kc, vc, tbl[:0], cu[:1], sp[:0]), {})]
+
+    def outcome(f, a, kw):
+        try:
+            r = f(*a, **kw)
+        except Exception as e:  # noqa: BLE001  (whatever a user would see)
+            return type(e), str(e)
+        lib.get_error()
+        r = r if isinstance(r, tuple) else (r,)
+        return [None if t is None else (t.dtype, tuple(t.shape), t.stride(), bits(t.bfloat16()).tolist()) for t in r]
+
+    from collections import Counter
+    kinds = Counter()
+    assert lib._torch_module() and lib._calls is not None
+    for f, a, kw in calls:
+        compiled = outcome(f, a, kw)
+        with monkeypatch.context() as m:
+            m.setattr(lib, "_calls", None)
+            python = outcome(f, a, kw)
+        assert compiled == python, (f.__name__, {n: x for n, x in kw.items()})
+        kinds[isinstance(compiled, list)] += 1
+    assert min(kinds.values()) > 20
+
+
 @pytest.mark.parametrize("D,heads,tokens", [(128, (8, 2), 1), (192, (8, 4), 1), (256, (4, 1), 3)])
 def test_waits_that_give_up_are_reported(lib, D, heads, tokens):
     """A decoding call whose key tiles never come: every warp gives up as one, the call ends,
