@@ -10,6 +10,7 @@ package fails if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from typing import Dict, Optional, Tuple
 
@@ -364,6 +365,14 @@ def _handle(stream, idx, torch):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _int64(v, name) -> int:
+    """v as the C call gets it; ctypes would wrap what does not fit."""
+    v = operator.index(v)
+    if not -2 ** 63 <= v < 2 ** 63:
+        raise ValueError(f"{name} must fit 64 bits, got {v}")
+    return v
+
+
 def _on_stream(handle, dev, torch):
     """Context in which tensors are allocated that belong to the stream `handle`."""
     # ExternalStream(0) is a new stream, not the default one
@@ -536,9 +545,11 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos=None
         raise ValueError("max_len must be at least 1")
     if window is not None and window < 1:
         raise ValueError("window must be at least 1")
+    max_len, window = _int64(max_len or 0, "max_len"), _int64(window or 0, "window")
+    key_block, key_stride = _int64(key_block, "key_block"), _int64(key_stride, "key_stride")
     if scale is None:
         scale = D ** -0.5
-    dims = ctypes.byref(cmp_attn_dims(B, T, Hq, Hk, D, qs, shape[0], shape[1], block_table.shape[1], max_len or 0))
+    dims = ctypes.byref(cmp_attn_dims(B, T, Hq, Hk, D, qs, shape[0], shape[1], block_table.shape[1], max_len))
     handle = _handle(stream, idx, torch)
 
     def allocate():
@@ -564,7 +575,7 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos=None
         with _on_stream(handle, dev, torch):
             out, lse, workspace = allocate()
     st = _on_device(idx, torch, lib.cmp_paged_attention, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                    block_table.data_ptr(), cu_seqlens.data_ptr(), _ptr(start_pos), scale, window or 0, key_block,
+                    block_table.data_ptr(), cu_seqlens.data_ptr(), _ptr(start_pos), scale, window, key_block,
                     key_stride, dt, out.data_ptr(), _ptr(lse), workspace.data_ptr(), workspace.nbytes, handle, dims)
     if st != CMP_OK:
         raise CmpError(st, "cmp_paged_attention")
@@ -573,7 +584,7 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos=None
 
 def paged_attention_workspace(T: int, Hq: int, Hk: int, D: int, max_len: Optional[int] = None) -> int:
     """Bytes of ``workspace`` a ``paged_attention`` call of these sizes needs on the current device."""
-    d = cmp_attn_dims(1, T, Hq, Hk, D, Hq * D, 1, 16, 1, max_len or 0)
+    d = cmp_attn_dims(*(_int64(v, "a size") for v in (1, T, Hq, Hk, D, Hq * D, 1, 16, 1, max_len or 0)))
     return int(lib.cmp_paged_attention_workspace(ctypes.byref(d)))
 
 

@@ -109,6 +109,15 @@ def test_workspace(cmp):
     assert cmp.paged_attention_workspace(1, 8, 2, 128, 1) <= cmp.paged_attention_workspace(4096, 8, 2, 128)
 
 
+def test_sizes_past_64_bits_are_refused(cmp):
+    """They would wrap to small ones."""
+    with pytest.raises(ValueError, match="64 bits"):
+        cmp.paged_attention_workspace(2 ** 64 + 4, 8, 2, 128)
+    with pytest.raises(ValueError, match="64 bits"):
+        cmp.paged_attention_workspace(4, 8, 2, 128, 2 ** 64 + 1)
+    assert cmp.paged_attention_workspace(2 ** 62, 8, 2, 128) == 0
+
+
 def test_binding_wants_cuda_tensors(cmp):
     import torch
     q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)

@@ -542,6 +542,18 @@ def test_both_bindings_agree(lib, monkeypatch):
     assert min(kinds.values()) > 20
 
 
+def test_numbers_past_64_bits_are_refused(lib):
+    """They would wrap to a small one (2^64 + 3 to a window of 3)."""
+    i = attn_inputs(34, [1], [70], 8, 2, 64, 16)
+    args = [b16(i.q, "bf16"), b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16"), dev(i.block_table), dev(i.cu_seqlens),
+            dev(i.start_pos)]
+    for name in ("max_len", "window", "key_block", "key_stride"):
+        for v in (2 ** 64 + 3, 2 ** 64, 2 ** 63, -2 ** 64 + 1):
+            with pytest.raises((ValueError, lib.CmpError)):
+                lib.paged_attention(*args, **{name: v})
+    assert lib.get_error() == 0
+
+
 @pytest.mark.parametrize("D,heads,tokens", [(128, (8, 2), 1), (192, (8, 4), 1), (256, (4, 1), 3)])
 def test_waits_that_give_up_are_reported(lib, D, heads, tokens):
     """A decoding call whose key tiles never come: every warp gives up as one, the call ends,
