@@ -16,7 +16,7 @@
 namespace cmp {
 cudaError_t launch_qk_norm_rope(const QkNormParams& p, cudaStream_t s, int sms);
 cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t s, int sms);
-cudaError_t kv_take_error(unsigned* word);
+cudaError_t kv_error_word(unsigned** word);
 cudaError_t launch_proj_tc(const Params& p, cudaStream_t s);
 cudaError_t launch_proj_decode(const Params& p, cudaStream_t s);
 bool proj_tc_supported(const Params& p);
@@ -265,6 +265,28 @@ void note_word_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64)
     g_word_devices.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+}
+
+// The words are shared by all streams of the device, so a kernel of another stream may
+// set bits at any time: each is read and cleared in one step.
+__device__ unsigned g_taken;
+__global__ void take_words_kernel(unsigned* kv, unsigned* decode, unsigned* chunk) {
+  g_taken = atomicExch(kv, 0u) | atomicExch(decode, 0u) | atomicExch(chunk, 0u);
+}
+
+// The current device's words, read and cleared, by way of stream s.
+cudaError_t take_device_words(cudaStream_t s, unsigned* word) {
+  static std::mutex mu;  // g_taken belongs to one call until it is read
+  std::lock_guard<std::mutex> lk(mu);
+  unsigned *kv, *decode, *chunk;
+  cudaError_t e = cmp::kv_error_word(&kv);
+  if (e == cudaSuccess) e = cmp::attn_decode_error_word(&decode);
+  if (e == cudaSuccess) e = cmp::attn_chunk_error_word(&chunk);
+  if (e != cudaSuccess) return e;
+  take_words_kernel<<<1, 1, 0, s>>>(kv, decode, chunk);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(word, g_taken, sizeof(*word), 0, cudaMemcpyDeviceToHost, s);
+  return e == cudaSuccess ? cudaStreamSynchronize(s) : e;
 }
 
 bool in(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
@@ -793,11 +815,9 @@ int cmp_get_error(void* stream) {
   if (cmp::noalloc_take_error(dev, &na) != CMP_OK) return CMP_ERR_CUDA;
   word |= na;
   if (dev < 64 && (g_word_devices.load(std::memory_order_relaxed) >> dev & 1)) {  // the paged cache operators' words
-    for (auto* take : {cmp::kv_take_error, cmp::attn_decode_take_error, cmp::attn_chunk_take_error}) {
-      unsigned v = 0;
-      if (take(&v) != cudaSuccess) return CMP_ERR_CUDA;
-      word |= v;
-    }
+    unsigned v = 0;
+    if (take_device_words(s, &v) != cudaSuccess) return CMP_ERR_CUDA;
+    word |= v;
   }
   if (word & cmp::kErrTimeout) return CMP_ERR_TIMEOUT;
   if (word & cmp::kErrIndex) return CMP_ERR_DEVICE_INDEX;

@@ -365,13 +365,13 @@ int attn_decode_rows(int64_t rows);
 int attn_decode_ctas(int D, int sms);
 cudaError_t launch_attn_decode(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s,
                                int ctas, int m);
-cudaError_t attn_decode_take_error(unsigned* word);
+cudaError_t attn_decode_error_word(unsigned** word);
 // Chunks: 128-row MMA tiles, one CTA per SM.
 int attn_chunk_rows(int D);      // rows per item
 int attn_chunk_key_tile(int D);  // keys per tile
 cudaError_t launch_attn_chunk(const AttnParams& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t s,
                               int ctas);
-cudaError_t attn_chunk_take_error(unsigned* word);
+cudaError_t attn_chunk_error_word(unsigned** word);
 cudaError_t launch_attn_combine(const AttnParams& p, int m, int ctas, cudaStream_t s);
 
 }  // namespace cmp

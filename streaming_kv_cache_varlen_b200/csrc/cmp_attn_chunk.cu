@@ -596,6 +596,6 @@ cudaError_t launch_attn_chunk(const AttnParams& p, const CUtensorMap& k, const C
   }
 }
 
-cudaError_t attn_chunk_take_error(unsigned* word) { return take_symbol_word(g_attn_err, word); }
+cudaError_t attn_chunk_error_word(unsigned** word) { return cudaGetSymbolAddress((void**)word, g_attn_err); }
 
 }  // namespace cmp

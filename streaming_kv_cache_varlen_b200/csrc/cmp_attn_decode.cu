@@ -459,7 +459,7 @@ cudaError_t launch_attn_decode(const AttnParams& p, const CUtensorMap& k, const 
   }
 }
 
-cudaError_t attn_decode_take_error(unsigned* word) { return take_symbol_word(g_attn_err, word); }
+cudaError_t attn_decode_error_word(unsigned** word) { return cudaGetSymbolAddress((void**)word, g_attn_err); }
 
 // Promotion to 128 bytes: a head's row is 3 lines at 192 channels, and its neighbours
 // are read much later (with 256 bytes the step above took 465 us).

@@ -218,19 +218,6 @@ struct KvAppendParams {
   float eps, inv_d;
 };
 
-// Reads and clears a __device__ error word on the current device (the caller has
-// synchronised the streams whose calls it wants covered).
-template <class W>
-inline cudaError_t take_symbol_word(W& symbol, unsigned* word) {
-  *word = 0;
-  unsigned v = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, symbol, sizeof(v));
-  const unsigned zero = 0;
-  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(symbol, &zero, sizeof(zero));
-  *word = v;
-  return e;
-}
-
 // Kernel launchers (each file defines its own).
 cudaError_t launch_sched(const Params& p, cudaStream_t s);
 cudaError_t launch_proj_mma(const Params& p, cudaStream_t s);

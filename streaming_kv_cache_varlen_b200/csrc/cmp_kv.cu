@@ -426,7 +426,7 @@ cudaError_t launch_kv_append(const KvAppendParams& p, cudaStream_t s, int sms) {
   return run_append<false, 32>(p, s, sms);
 }
 
-// The error word of the current device's kv_append calls, read and cleared.
-cudaError_t kv_take_error(unsigned* word) { return take_symbol_word(g_kv_err, word); }
+// The error word of the current device's kv_append calls.
+cudaError_t kv_error_word(unsigned** word) { return cudaGetSymbolAddress((void**)word, g_kv_err); }
 
 }  // namespace cmp

@@ -554,6 +554,44 @@ def test_numbers_past_64_bits_are_refused(lib):
     assert lib.get_error() == 0
 
 
+def test_error_words_are_taken_once(lib):
+    """Threads that ask for errors on streams of their own while another one's calls report
+    them: each report is taken by exactly one of them (a token of one head of 16 channels is
+    one warp's, which reports once), and none is lost."""
+    import threading
+
+    import torch
+    i = make_paged_inputs(seed=35, lens=[1], ctx=[3], Hq=1, Hk=1, D=16, page=16)
+    args = (b16(i.k, "bf16"), b16(i.v, "bf16"), b16(i.k_cache, "bf16"), b16(i.v_cache, "bf16"))
+    good, bad, cu, sp = dev(i.block_table), dev(i.block_table * 0 - 1), dev(i.cu_seqlens), dev(i.start_pos)
+    lib.kv_append(*args, good, cu, sp)
+    torch.cuda.synchronize()
+    assert lib.get_error() == 0
+    stop, seen = threading.Event(), []
+
+    def ask():
+        s, n = torch.cuda.Stream(), 0
+        while not stop.is_set():
+            n += lib.get_error(s) == 5
+        seen.append(n)
+
+    askers = [threading.Thread(target=ask) for _ in range(3)]
+    for t in askers:
+        t.start()
+    s = torch.cuda.Stream()
+    mine, rounds = 0, 400
+    for _ in range(rounds):
+        lib.kv_append(*args, bad, cu, sp, stream=s)
+        got = lib.get_error(s)
+        assert got in (0, 5)
+        mine += got == 5
+        assert lib.get_error(s) == 0
+    stop.set()
+    for t in askers:
+        t.join()
+    assert mine + sum(seen) == rounds and lib.get_error() == 0
+
+
 @pytest.mark.parametrize("D,heads,tokens", [(128, (8, 2), 1), (192, (8, 4), 1), (256, (4, 1), 3)])
 def test_waits_that_give_up_are_reported(lib, D, heads, tokens):
     """A decoding call whose key tiles never come: every warp gives up as one, the call ends,
