@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import operator
 import os
+import warnings
 from typing import Dict, Optional, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -278,7 +279,7 @@ _torch = None
 _DTYPE = {}  # torch dtype -> CMP_NSA_FP16 / CMP_NSA_BF16
 
 
-_calls = None  # binding/fast.cpp; None with another library than the one it links
+_calls = None  # binding/fast.cpp, if it may be used
 
 
 # The paged operators' calls are short (a decode step's append takes 5 us on the device), so
@@ -286,16 +287,28 @@ _calls = None  # binding/fast.cpp; None with another library than the one it lin
 # returns -1, having done nothing, for every other call; the code below it then handles that
 # or says what is wrong.
 
+def _compiled_calls(torch):
+    """binding/fast.cpp, or None: with another library than the one it links, and (with a
+    warning) where it was not built for this PyTorch. The functions then do without it."""
+    if os.environ.get("CMP_LIBRARY"):
+        return None
+    try:
+        from . import _fast
+        why = f"it was built for PyTorch {getattr(_fast, 'torch_version', 'of another version')}"
+        if getattr(_fast, "torch_version", None) == torch.__version__:
+            return _fast
+    except ImportError as e:
+        why = str(e)
+    warnings.warn(f"the paged operators run without their compiled binding (10 us more per call): {why}; "
+                  "build it with `python -c 'import __graft_entry__ as g; g.build()'`", RuntimeWarning, stacklevel=3)
+    return None
+
+
 def _torch_module():
     global _torch, _calls
     if _torch is None:
         import torch
-        if not os.environ.get("CMP_LIBRARY"):
-            if not os.path.exists(os.path.join(_PKG, "_fast.so")):
-                raise ImportError("_fast.so is missing: build it with "
-                                  "`python -c 'import __graft_entry__ as g; g.build()'`")
-            from . import _fast
-            _calls = _fast
+        _calls = _compiled_calls(torch)
         _DTYPE.update({torch.float16: 0, torch.bfloat16: 1})
         _torch = torch
     return _torch

@@ -118,6 +118,80 @@ def test_sizes_past_64_bits_are_refused(cmp):
     assert cmp.paged_attention_workspace(2 ** 62, 8, 2, 128) == 0
 
 
+def refuses_as_ever(cmp, monkeypatch):
+    """The operators with their compiled binding looked for anew."""
+    import torch
+    for name in ("_torch", "_calls"):
+        monkeypatch.setattr(cmp, name, None)
+    with pytest.warns(RuntimeWarning, match="compiled binding"):
+        with pytest.raises(ValueError, match="CUDA"):
+            cmp.qk_norm_rope(torch.zeros(2, 4, 64, dtype=torch.bfloat16), None, torch.ones(64, dtype=torch.bfloat16))
+    assert cmp._calls is None
+
+
+def test_without_the_compiled_binding(cmp, monkeypatch):
+    """A missing one is no reason to refuse a call: the Python one serves every call."""
+    import sys
+    monkeypatch.delattr(cmp, "_fast", raising=False)
+    monkeypatch.setitem(sys.modules, cmp.__name__ + "._fast", None)
+    refuses_as_ever(cmp, monkeypatch)
+
+
+def test_compiled_binding_of_another_pytorch(cmp, monkeypatch):
+    """One that was built against other headers would read tensors wrongly: it is not used."""
+    import sys
+    import types
+    for other in (types.SimpleNamespace(torch_version="1.0.0"), types.SimpleNamespace()):
+        monkeypatch.setattr(cmp, "_fast", other, raising=False)
+        monkeypatch.setitem(sys.modules, cmp.__name__ + "._fast", other)
+        refuses_as_ever(cmp, monkeypatch)
+
+
+def test_compiled_binding_of_this_pytorch(cmp, monkeypatch):
+    import torch
+    for name in ("_torch", "_calls"):
+        monkeypatch.setattr(cmp, name, None)
+    assert cmp._torch_module() is torch and cmp._calls.torch_version == torch.__version__
+
+
+def test_build_without_pytorch(monkeypatch, tmp_path):
+    """The library needs no PyTorch to be built; its compiled binding is left out then, and where
+    its compilation fails."""
+    import importlib.util
+    import os
+
+    import streaming_kv_cache_varlen_b200 as m
+    spec = importlib.util.spec_from_file_location("build_script", os.path.join(os.path.dirname(m.__file__), "_build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    with monkeypatch.context() as p:
+        p.setattr(b.importlib.util, "find_spec", lambda name: None)
+        assert b.build_fast(force=True) is None
+    monkeypatch.setattr(b, "FAST", str(tmp_path / "fast.so"))
+    monkeypatch.setattr(b, "OBJDIR", str(tmp_path))
+    monkeypatch.setattr(b, "FAST_KEY", str(tmp_path / "fast.key"))
+    bad = tmp_path / "bad.cpp"
+    bad.write_text("#error no\n")
+    monkeypatch.setattr(b, "FAST_SRC", str(bad))
+    with pytest.warns(UserWarning, match="not built"):
+        assert b.build_fast() is None
+    ok = tmp_path / "ok.cpp"
+    ok.write_text("int x;\n")
+    monkeypatch.setattr(b, "FAST_SRC", str(ok))
+    assert b.build_fast() == b.FAST and os.path.exists(b.FAST)
+    stamp = os.stat(b.FAST).st_mtime_ns
+    assert b.build_fast() == b.FAST and os.stat(b.FAST).st_mtime_ns == stamp   # up to date
+    monkeypatch.setattr(b, "FAST_SRC", str(bad))
+    with pytest.warns(UserWarning, match="not built"):
+        assert b.build_fast(force=True) is None
+    assert not os.path.exists(b.FAST)                                           # nor is the old one left
+    monkeypatch.setattr(b, "FAST_SRC", str(ok))
+    assert b.build_fast() == b.FAST
+    stamp = os.stat(b.FAST).st_mtime_ns
+    (tmp_path / "fast.key").write_text("another PyTorch")
+    assert b.build_fast() == b.FAST and os.stat(b.FAST).st_mtime_ns != stamp   # built anew
+
+
 def test_binding_wants_cuda_tensors(cmp):
     import torch
     q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
