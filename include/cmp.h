@@ -357,7 +357,7 @@ CMP_API int cmp_kv_append(const void* k, const void* v, const void* norm_weight,
                           int32_t dtype, void* k_cache, void* v_cache, void* stream, const cmp_kv_dims* dims);
 
 typedef struct cmp_attn_dims {
-  int64_t B;             /* sequences */
+  int64_t B;             /* sequences, at most 2^20 */
   int64_t T;             /* tokens: rows of q; T * Hq <= INT32_MAX */
   int64_t Hq, Hk;        /* query heads 1..1024, key heads 1..256; Hq = G * Hk with G <= 128 */
   int64_t D;             /* channels per head, a multiple of 16, at most 256 */

@@ -316,7 +316,7 @@ int check_rope(const cmp_rope* r, int64_t D, cmp::RopeTable* o) {
 
 int check_attn_dims(const cmp_attn_dims* d) {
   if (!d) return CMP_ERR_NULLPTR;
-  if (!in(d->B, 0, INT32_MAX - 1) || !in(d->T, 0, INT32_MAX - 1) || !in(d->Hq, 1, 1024) || !in(d->Hk, 1, 256) ||
+  if (!in(d->B, 0, cmp::kMaxSequences) || !in(d->T, 0, INT32_MAX - 1) || !in(d->Hq, 1, 1024) || !in(d->Hk, 1, 256) ||
       d->Hq % d->Hk || d->Hq / d->Hk > 128 || !valid_head_dim(d->D) || d->T * d->Hq > INT32_MAX ||
       !valid_stride(d->q_stride, d->Hq, d->D) || !in(d->page_size, 16, 1024) || d->page_size % 16 ||
       !in(d->block_num, 1, INT32_MAX / d->page_size) || !in(d->table_stride, 1, INT32_MAX) ||

@@ -104,6 +104,11 @@ def test_attention_refusals(cmp):
     assert need > 0 and attn(cmp, ws_bytes=need - 1) == 2
 
 
+def test_attention_sequences(cmp):
+    assert attn(cmp, B=2 ** 20 + 1) == 2 and attn(cmp, B=2 ** 30) == 2
+    assert attn(cmp, {"q": None}, B=2 ** 20) == 1                 # the sizes are fine
+
+
 def test_workspace(cmp):
     assert cmp.paged_attention_workspace(4, 8, 2, 40) == 0
     assert cmp.paged_attention_workspace(1, 8, 2, 128, 1) <= cmp.paged_attention_workspace(4096, 8, 2, 128)

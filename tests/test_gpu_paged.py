@@ -356,6 +356,24 @@ def test_many_sequences(lib, max_len):
     attn_case(lib, attn_inputs(16, lens, [int(x) for x in rng.integers(0, 90, 1200)], 4, 2, 64, 16), max_len=max_len)
 
 
+@pytest.mark.parametrize("lens,ctx", [([1, 2, 1], [20000, 30, 20300]), ([40, 1, 300], [6200, 30, 6100])])
+def test_most_sequences(lib, lens, ctx):
+    """As many sequences as a call may have, three of them with tokens: what those three give
+    alone. The contexts are such that a CTA's part holds the end of one and the begin of the next."""
+    import torch
+    B, at = 2 ** 20, [0, 700001, 2 ** 20 - 1]
+    i = attn_inputs(17, lens, ctx, 4, 1, 64, 128)
+    out, lse, args = attn_case(lib, i)
+    cu, sp = np.zeros(B + 1, np.int32), np.zeros(B, np.int32)
+    tbl = np.full((B, i.block_table.shape[1]), -1, np.int32)
+    for b, n, t, c in zip(at, lens, i.block_table, i.start_pos):
+        cu[b + 1], tbl[b], sp[b] = n, t, c
+    cu = np.cumsum(cu).astype(np.int32)
+    o, l = lib.paged_attention(*args[:3], dev(tbl), dev(cu), dev(sp), max_len=max(lens), return_lse=True)
+    assert lib.get_error() == 0
+    assert torch.equal(o, out) and torch.equal(l, lse)
+
+
 def test_strided_queries(lib):
     import torch
     i = attn_inputs(2, [40, 1], [100, 500], 8, 2, 128, 64)
