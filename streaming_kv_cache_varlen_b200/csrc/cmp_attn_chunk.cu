@@ -63,12 +63,23 @@ struct ChunkBars {
   uint64_t piece_full[kPieces], piece_empty[kPieces];
 };
 
-// A piece as the roles read it.
+// Key tiles that are summed in the accumulator before they leave it. The tensor core cuts
+// sums off instead of rounding them, up to 2^-23 of the accumulator for each 16 keys, always
+// towards zero: a row of 2^20 keys lost 0.6 % in one go. The parts of a longer piece are
+// added in fp32 (rounded) in the piece's slot of the workspace, at 2^-12 each at most.
+constexpr int kPartTiles = 256;
+
+// Kinds of parts: the first of the piece, the part after which the item's rows are complete
+// (no other CTA has a piece of it), part of a piece that begins the item.
+constexpr uint32_t kPartFirst = 1, kPartEnd = 2, kPartBegins = 4;
+
+// A part of a piece (most have one) as the roles read it.
 struct ChunkPiece {
-  AttnPiece o;
-  int last_cta;    // of its item (a piece that begins an item and does not end it)
-  int tok0, rem0;  // row0 = tok0 * G + rem0
-  bool valid;      // false: the CTA's part ends here
+  AttnPiece o;         // [j0, j1): the part's tiles
+  int last_cta;        // of its item (a piece that begins an item and does not end it; else 0)
+  int tok0, rem0;      // row0 = tok0 * G + rem0
+  uint32_t kind;       // kPart...
+  bool valid;          // false: the CTA's share of the work ends here
 };
 
 // The largest of three; NaN if one of them is.
@@ -76,6 +87,43 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// Adds what this thread left of its row in the workspace to the accumulator in TMEM and to
+// the row's reference and sum; part: its first four channels there, `stride` floats apart
+// from the next four. A call, as its registers in line made the usual pieces' stores slower
+// (4000 tokens over compressed rows 129 us instead of 124.5).
+__device__ __noinline__ float2 add_part(uint32_t o_t, const float* part, int stride, const float* ml_at, int D, bool mine,
+                                        float ref, float l) {
+  float w_old = 0.f, w_new = 1.f;
+  if (mine) {
+    const float2 ml = *reinterpret_cast<const float2*>(ml_at);
+    const float m = fmaxf(ml.x, ref), at = m == neg_inf() ? 0.f : m;
+    w_old = ex2(ml.x - at);
+    w_new = ex2(ref - at);
+    l = fmaf(ml.y, w_old, l * w_new);
+    ref = m;
+  }
+#pragma unroll 1
+  for (int d = 0; d < D; d += 16) {
+    uint32_t a[16];
+    sm100::tmem_ld16(o_t + d, a);
+    sm100::tmem_ld_wait16(a);
+    if (mine) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(part + (int64_t)((d + e) / 4) * stride);
+        a[e] = __float_as_uint(fmaf(x.x, w_old, __uint_as_float(a[e]) * w_new));
+        a[e + 1] = __float_as_uint(fmaf(x.y, w_old, __uint_as_float(a[e + 1]) * w_new));
+        a[e + 2] = __float_as_uint(fmaf(x.z, w_old, __uint_as_float(a[e + 2]) * w_new));
+        a[e + 3] = __float_as_uint(fmaf(x.w, w_old, __uint_as_float(a[e + 3]) * w_new));
+      }
+    }
+    __syncwarp();
+    sm100::tmem_st16(o_t + d, a);
+  }
+  sm100::tmem_st_wait();
+  return make_float2(ref, l);
 }
 
 template <bool BF16, int DP>
@@ -136,16 +184,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         AttnWalk<KT, C::kM> walk(p);
         walk.begin(start.units, start.b, start.h, start.qt, start.off);
         const int64_t share = start.share;
+        AttnPiece o;
+        int j = 0, j1 = 0;  // tiles of the piece that no part has yet
         for (int i = 0;; ++i) {
           const int s = i % kPieces;
           if (i >= kPieces &&
               !sm100::mbar_wait(&bars.piece_empty[s], (uint32_t)(i / kPieces - 1) & 1u, &abort_flag))
             break;
           ChunkPiece& c = pieces[s];
-          AttnPiece o;
-          const bool valid = walk.next(o);
+          bool valid = true;
+          const bool first = j == j1;
+          if (first) {
+            valid = walk.next(o);
+            j = o.j0;
+            j1 = o.j1;
+          }
           if (valid) {
             c.o = o;
+            c.o.j0 = j;
+            j = min(j + kPartTiles, j1);
+            c.o.j1 = j;
+            c.kind = (first ? kPartFirst : 0) | (o.whole() && j == j1 ? kPartEnd : 0) | (o.j0 == o.T0 ? kPartBegins : 0);
+            c.last_cta = 0;
             if (o.j0 == o.T0 && !o.whole()) c.last_cta = attn_last_cta(blockIdx.x, share, o);
             c.tok0 = p.div_g.div(o.row0);
             c.rem0 = o.row0 - c.tok0 * p.G;
@@ -355,7 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int pi = 0; ok && c->valid; ++pi) {
       const int row = w * kRows + r;  // of the item
       const bool mine = row < c->o.rows;
-      if (tid == 0 && !c->o.whole() && c->o.j0 == c->o.T0) {
+      const uint32_t kind = c->kind;
+      if (tid == 0 && (kind & kPartFirst) && c->last_cta) {
         attn_write_desc(p, blockIdx.x, c->last_cta, &c->o);
         begun = true;
       }
@@ -500,16 +561,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         sm100::tc_fence_after();
         if (warp_rows) {
-          const bool whole = c->o.whole();
+          const bool finish = kind & kPartEnd;
+          // slot 1 is also where the parts of a whole item are added: the piece that a CTA
+          // begins and does not end is its last one
+          const int64_t slot = (int64_t)blockIdx.x * 2 + ((kind & kPartBegins) ? 1 : 0);
+          if (!(kind & kPartFirst)) {
+            const float2 ml = add_part(o_t, attn_chunk_part(p, DP, C::kM, slot, 0, row), C::kM * 4,
+                                       p.part_ml + (slot * C::kM + row) * 2, p.D, mine, ref, l);
+            ref = ml.x;
+            l = ml.y;
+          }
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          const int64_t slot = (int64_t)blockIdx.x * 2 + (c->o.j0 > c->o.T0 ? 0 : 1);
           unsigned char* orow_s = qw + r * 128;  // whole rows pass through the warp's part of the Q tile
 #pragma unroll
           for (int d = 0; d < DP; d += 32) {
             uint32_t a[32];
             sm100::tmem_ld32(o_t + d, a);
             sm100::tmem_ld_wait(a);
-            if (whole) {
+            if (finish) {
 #pragma unroll
               for (int e = 0; e < 32; e += 8) {
                 uint32_t v[4];
@@ -529,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (whole) {
+          if (finish) {
             __syncwarp();
             const int rows = c->o.rows, rem0 = c->rem0, qrow = fresh();
             uint16_t* base =
@@ -547,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (mine) {
-            if (!whole) *reinterpret_cast<float2*>(p.part_ml + (slot * C::kM + row) * 2) = make_float2(ref, l);
+            if (!finish) *reinterpret_cast<float2*>(p.part_ml + (slot * C::kM + row) * 2) = make_float2(ref, l);
             else if (p.lse) p.lse[out_row()] = attn_lse(ref, l);
           }
         }

@@ -610,6 +610,82 @@ def test_error_words_are_taken_once(lib):
     assert mine + sum(seen) == rounds and lib.get_error() == 0
 
 
+def long_call(seed, lens, ctx, Hq, Hk, D, dtype, blocks, page=512, ones=False):
+    """Sequences over one cache of few blocks, each sequence's table repeating them in its own order."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    dt = torch.float16 if dtype == "fp16" else torch.bfloat16
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    kc = (rand(blocks, page, Hk, D) * 0.5).to(dt)
+    vc = torch.ones_like(kc) if ones else rand(blocks, page, Hk, D).to(dt)
+    q = rand(sum(lens), Hq, D).to(dt)
+    pages = max(-(-(n + c) // page) for n, c in zip(lens, ctx))
+    tbl = torch.stack([torch.randperm(blocks, generator=g, device="cuda").repeat(-(-pages // blocks))[:pages]
+                       for _ in lens]).int()
+    cu = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32, device="cuda")
+    return q, kc, vc, tbl, cu, torch.tensor(ctx, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("keys", [2 ** 15, 2 ** 20])
+def test_long_sums_keep_their_size(lib, D, keys):
+    """Values of 1 come out as 1 however many keys a CTA sums (more items than CTAs). The sums of
+    the weights, rounded to fp16 (h relative), lose at most 2^-12 in the accumulator, and the sum
+    that they are divided by is off by (tiles of a part + 64) 2^-24; out is rounded once (h)."""
+    args = long_call(D, [17] * 10, [keys - 17] * 10, 128, 16, D, "fp16", 2, ones=True)
+    out, lse = lib.paged_attention(*args, max_len=17, return_lse=True)
+    assert lib.get_error() == 0
+    h = 2.0 ** -11
+    err = float((out.double() - 1).abs().max())
+    assert err <= (h + h + 2.0 ** -12 + 320 * 2.0 ** -24) * 1.001, err
+
+
+@pytest.mark.parametrize("D,G,dtype", [(64, 17, "bf16"), (128, 17, "fp16"), (128, 129, "bf16"), (192, 40, "fp16"),
+                                       (192, 17, "bf16"), (256, 17, "fp16")])
+@pytest.mark.parametrize("window", [0, 33000])
+def test_pieces_of_several_parts(lib, D, G, dtype, window):
+    """Contexts around the multiples of what is summed in one go (256 tiles of 128 or 64 keys),
+    more items than CTAs: whole items in parts, cut ones in parts, and short ones between them."""
+    import torch
+    from tests.paged_helpers import HALF, TINY, U
+    part = 256 * (128 if D <= 128 else 64)
+    if G > 128:
+        G, lens = 16, [9, 2, 16]
+    else:
+        lens = [1, 1, 1]
+    ctx = [part - 1, part, part + 1, 2 * part - 2, 2 * part + 130, 40, 3 * part + 5, 7]
+    ctx, lens = (ctx * 24)[:180], (lens * 60)[:180]
+    args = long_call(D + G, lens, ctx, G, 1, D, dtype, 4)
+    q, kc, vc, tbl, cu, sp = args
+    out, lse = lib.paged_attention(*args, max_len=max(max(lens), 2), window=window or None, return_lse=True)
+    again, lse2 = lib.paged_attention(*args, max_len=max(max(lens), 2), window=window or None, return_lse=True)
+    assert lib.get_error() == 0
+    assert torch.equal(again, out) and torch.equal(lse2, lse)
+    h, scale = HALF[dtype], D ** -0.5
+    k64, v64 = kc.double().view(-1, D), vc.double().view(-1, D)
+    worst = worst_lse = 0.0
+    for b in [*range(8), 100, 179]:
+        for t in (0, lens[b] - 1):
+            row = int(cu[b]) + t
+            n = ctx[b] + t + 1
+            lo = max(0, n - window) if window else 0
+            at = torch.arange(lo, n, device="cuda")
+            at = tbl[b].long()[at // 512] * 512 + at % 512
+            x = q[row].double() @ k64[at].t() * scale
+            mag = (q[row].double().abs() @ k64[at].abs().t() * scale).amax(-1)
+            want_lse = torch.logsumexp(x, -1)
+            w = torch.exp(x - want_lse[:, None])
+            want, vm = w @ v64[at], w @ v64[at].abs()
+            dw = (2 * D + 8) * U * mag + 8 * U
+            m = n - lo + 64
+            lim = h * want.abs() + vm * (h + 2 * dw + 4 * m * U)[:, None] * (1 + h) + TINY[dtype] * (
+                1 + v64[at].abs().sum(0))
+            worst = max(worst, float(((out[row].double() - want).abs() / lim).max()))
+            worst_lse = max(worst_lse, float(((lse[row].double() - want_lse).abs() /
+                                              (dw + m * U + 4 * U * want_lse.abs())).max()))
+    assert worst <= 1 and worst_lse <= 1, (worst, worst_lse)
+
+
 @pytest.mark.parametrize("D,heads,tokens", [(128, (8, 2), 1), (192, (8, 4), 1), (256, (4, 1), 3)])
 def test_waits_that_give_up_are_reported(lib, D, heads, tokens):
     """A decoding call whose key tiles never come: every warp gives up as one, the call ends,
