@@ -65,7 +65,7 @@ struct ChunkBars {
 
 // Key tiles that are summed in the accumulator before they leave it. The tensor core cuts
 // sums off instead of rounding them, up to 2^-23 of the accumulator for each 16 keys, always
-// towards zero: a row of 2^20 keys lost 0.6 % in one go. The parts of a longer piece are
+// towards zero: a row of 2^20 keys lost 0.7 % in one go. The parts of a longer piece are
 // added in fp32 (rounded) in the piece's slot of the workspace, at 2^-12 each at most.
 constexpr int kPartTiles = 256;
 

@@ -308,13 +308,20 @@ __global__ void __launch_bounds__(DecodeCfg<DP, NB>::kThreads, DecodeCfg<DP, NB>
               pf[b][0] = transpose8(pack2<BF16>(x[b][0], x[b][1]));
               pf[b][1] = transpose8(pack2<BF16>(x[b][2], x[b][3]));
             }
-            // O^T += V^T P^T
+            // O^T += V^T P^T, added outside the product: the tensor core cuts its fp32 sums
+            // off, always towards zero, which over 2^22 keys lost 0.7 % of a row (the
+            // additions cost nothing at 8 rows per item, at most 1 % at 16)
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
               uint32_t a[4];
               ldsm4t(va + (s >> 2) * (kKT * 128) + voff[s & 3], a);
 #pragma unroll
-              for (int b = 0; b < NB; ++b) mma16816<BF16>(acc[s][b], a, pf[b][0], pf[b][1]);
+              for (int b = 0; b < NB; ++b) {
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816<BF16>(t, a, pf[b][0], pf[b][1]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[s][b][e] += t[e];
+              }
             }
           }
           __syncwarp();

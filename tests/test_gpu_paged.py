@@ -640,6 +640,21 @@ def test_long_sums_keep_their_size(lib, D, keys):
     assert err <= (h + h + 2.0 ** -12 + 320 * 2.0 ** -24) * 1.001, err
 
 
+@pytest.mark.parametrize("D", [64, 128, 192, 256])
+@pytest.mark.parametrize("heads", [2, 16])
+def test_long_sums_of_decoding_keep_their_size(lib, D, heads):
+    """The same of single tokens over 2^22 keys, 8 and 16 rows per item. A warp adds 2^16 times
+    and rounds each sum, which errs to either side (at most 6 sqrt(2^16) 2^-24 but for one row in
+    10^8), in the numerator and in the denominator; within 16 keys it may cut 16 times."""
+    keys = 2 ** 22
+    args = long_call(D, [1] * 20, [keys - 1] * 20, 16 * heads, 16, D, "fp16", 2, ones=True)
+    out = lib.paged_attention(*args, max_len=1)
+    assert lib.get_error() == 0
+    h, u = 2.0 ** -11, 2.0 ** -24
+    err = float((out.double() - 1).abs().max())
+    assert err <= (h + h + 2 * 6 * 2 ** 8 * u + 32 * u) * 1.001, err
+
+
 @pytest.mark.parametrize("D,G,dtype", [(64, 17, "bf16"), (128, 17, "fp16"), (128, 129, "bf16"), (192, 40, "fp16"),
                                        (192, 17, "bf16"), (256, 17, "fp16")])
 @pytest.mark.parametrize("window", [0, 33000])
