@@ -272,7 +272,7 @@ CMP_API int cmp_nsa_compress(const void* input, const void* weight, const int32_
  * (dtype CMP_NSA_FP16 or CMP_NSA_BF16) and on a pair of paged caches, k_cache and
  * v_cache [block_num, page_size, Hk, D]: the layout of cmp_nsa_compress's paged
  * input, so the cache that cmp_kv_append fills is one that cmp_nsa_compress
- * compresses. Position p of sequence b is row p % page_size of block
+ * compresses (with pages of 64 or 128 rows). Position p of sequence b is row p % page_size of block
  * block_table[b][p / page_size]. Packed tokens: sequence b owns rows
  * cu_seqlens[b] .. cu_seqlens[b+1]-1 at positions start_pos[b], start_pos[b]+1, ...
  *
@@ -285,10 +285,12 @@ CMP_API int cmp_nsa_compress(const void* input, const void* weight, const int32_
  * size). None of the three uses the library's per-stream workspace or allocates
  * memory, so they may be captured at any time and run on several streams at once.
  * What their kernels find wrong (cu_seqlens not rising from 0 or past T, a
- * negative start_pos, positions past INT32_MAX, a needed table entry outside
- * [0, block_num) or past table_stride) never faults: the access is skipped and an
- * error word of the device is set, which cmp_get_error reports (on any stream of
- * that device) and clears. B == 0 or T == 0 is a successful no-op. */
+ * negative start_pos, positions past INT32_MAX - 1 when appending and past
+ * INT32_MAX - 1024 when attending, a needed table entry outside [0, block_num) or
+ * past table_stride) never faults: the access is skipped and an error word of the
+ * device is set, which cmp_get_error reports (on any stream of that device) and
+ * clears. T == 0 is a successful no-op, with B == 0 too; tokens without any sequence
+ * (B == 0, T > 0) are CMP_ERR_INVALID. */
 
 /* The position rotation of the last `dim` channels of a head (cmp_compressor's
  * tables, one row per token):
@@ -317,7 +319,8 @@ typedef struct cmp_qk_dims {
 
 /* Norms of queries and keys for each head with the position rotation in the same
  * pass: y = x / sqrt(mean(x^2) + eps) * weight over a head's D channels, then the
- * rotation; fp32 inside, one rounding to dtype.
+ * rotation; fp32 inside, one rounding to dtype. Heads whose squares leave fp32's
+ * range (bf16 holds them) are normed in range.
  *   q, k            device [T, Hq, D], [T, Hk, D]; k, k_weight, k_out unused if Hk == 0
  *   q_weight, k_weight  device [D], dtype
  *   rope            host pointer, NULL: no rotation
@@ -336,7 +339,8 @@ typedef struct cmp_kv_dims {
   int64_t D;                   /* channels per head, a multiple of 16, at most 256 */
   int64_t k_stride, v_stride;  /* elements from one token to the next */
   int64_t block_num;           /* blocks of each cache; block_num * page_size <= INT32_MAX */
-  int64_t page_size;           /* rows per block, 1..1024 */
+  int64_t page_size;           /* rows per block, 1..1024 (cmp_paged_attention reads pages that are
+                                  multiples of 16 only) */
   int64_t table_stride;        /* columns of block_table */
 } cmp_kv_dims;
 
@@ -375,13 +379,16 @@ typedef struct cmp_attn_dims {
  * of those the last `window` if window > 0:
  *   key_block = key_stride = 1: plain causal attention; the cache holds the chunk's
  *     own keys too (cmp_kv_append comes before);
- *   key_block = key_stride = ratio: rows that the Compressor made of `ratio` positions;
- *   key_block = compress_block_size, key_stride = compress_stride: NSA's rows.
+ *   key_block = compress_block_size, key_stride = compress_stride: NSA's rows;
+ *   key_block = key_stride = r: rows that each stand for r positions of their own.
+ * (cmp_compressor's rows of C4A and C128A are not among them: they have 512 channels
+ * and come packed, not paged.)
  *   out = sum_j softmax_j(scale q.k_j) v_j,  lse = ln sum_j exp(scale q.k_j)
  * A row that sees no key gets out = 0, lse = -inf. lse joins attentions over
  * different caches (raw and compressed rows, windows): the weights exp(lse_i - lse)
  * of their outs. Scores, statistics and sums are fp32; the weights are rounded to
- * dtype before the product with v, and out once at the end.
+ * dtype before the product with v, and out once at the end. Rounding out aside, an
+ * output is off by at most about half a step of dtype of sum_j softmax_j |v_j|.
  *   q            device [T, Hq, D];  out  device [T, Hq, D], dense
  *   k_cache, v_cache  device [block_num, page_size, Hk, D]; rows that no token of
  *                the call sees may hold anything (NaN too). Inside one call a
@@ -396,8 +403,8 @@ typedef struct cmp_attn_dims {
  *                aligned; its contents need no preparation and mean nothing afterwards.
  *                Calls that may overlap need one each.
  * A sequence longer than max_len, whose cu_seqlens or start_pos entries are not
- * usable, or with positions past INT32_MAX - 1024 is skipped and reported (its rows are left as they were); a missing
- * table entry reads as zeros and is reported. Results do not depend on timing
+ * usable, or with positions past INT32_MAX - 1024 is skipped and reported (its rows
+ * are left as they were); a missing table entry reads as zeros and is reported. Results do not depend on timing
  * (no floating-point atomics).
  * Returns CMP_OK, CMP_ERR_NULLPTR, CMP_ERR_INVALID, CMP_ERR_UNSUPPORTED (dtype) or
  * CMP_ERR_CUDA (launch, or the driver cannot describe the cache as a TMA tensor). */

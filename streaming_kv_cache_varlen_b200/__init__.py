@@ -533,8 +533,9 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos=None
     ``scale`` defaults to 1 / sqrt(D); ``max_len`` is the most tokens any sequence of the
     call has (default T: give it, so that decoding is known as such); ``window`` the
     keys a token sees at most; ``key_block`` / ``key_stride`` describe caches of compressed
-    rows. ``workspace``: a CUDA tensor of at least ``paged_attention_workspace`` bytes
-    (allocated per call by default)."""
+    rows. D is a multiple of 16, at most 256. ``workspace``: a CUDA tensor of at least
+    ``paged_attention_workspace`` bytes (allocated per call by default). What a call with a
+    ``stream`` allocates belongs to that stream."""
     torch = _torch or _torch_module()
     if stream is None and _calls is not None:
         r = _calls.paged_attention(q, k_cache, v_cache, block_table, cu_seqlens, start_pos, scale, max_len, window,

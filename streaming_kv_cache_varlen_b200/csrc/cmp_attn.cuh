@@ -18,6 +18,11 @@
 // softmax statistics in the workspace (a CTA leaves at most two: slot 0 for an
 // item begun by an earlier CTA, slot 1 for one that it begins and does not end),
 // and attn_combine_kernel joins them in the order of the keys.
+//
+// Roundings to 16 bits: the weights, before their product with V (the tensor core
+// takes both factors in one 16-bit type; fp32 weights would cost a second product,
+// half as much again in chunks, for an error below out's own rounding), and out. Each
+// weight is off by at most half a step, to either side; their sum l stays fp32.
 #pragma once
 
 #include "cmp_internal.cuh"

@@ -21,9 +21,11 @@
 // Bound by the chain scores - softmax - weights - products of a row tile, of which two
 // run in turn: 128 keys of a pair of tiles take 3400 clocks, of which the tensor core
 // works 2050 and the special function unit 2050 (16 exponentials a clock). 4096 tokens
-// of 32 heads of 128 over 16384 positions (962 GFLOP) take 715 us, 0.82 of the measured
-// matrix product burst (845 us back to back, where power limits the clock). Measured and not kept: 2^x by polynomial for 1/8 to 3/8 of the
-// weights (as fast or slower: its 15 instructions a pair take the issue slots that the
+// of 32 heads of 128 over 16384 positions (962 GFLOP) take 726 us, 0.81 of the measured
+// matrix product burst (842 to 847 us back to back, where power limits the clock).
+// The running reference and sum of a softmax in one pass: Milakov and Gimelshein, Online
+// normalizer calculation for softmax (2018). Measured and not kept: 2^x by polynomial for
+// 1/8 to 3/8 of the weights (as fast or slower: its 15 instructions a pair take the issue slots that the
 // special function unit leaves), half a row per thread on 16 softmax warps (800 us: a
 // second pass over TMEM, as 64 scores and the rest do not fit 104 registers), tiles of
 // 64 keys with two score buffers (800 to 950 us: the fixed cost of a step, 500 clocks,

@@ -11,7 +11,7 @@
 //   S^T = K Q^T,  O^T += V^T P^T
 // (with the queries as rows, an item of 8 rows or fewer spent twice the products and
 // registers, and a warp has little else to overlap them with: 635 us for 128
-// sequences of 24 key heads of 192, two query heads each, where this takes 418, 0.93
+// sequences of 24 key heads of 192, two query heads each, where this takes 419, 0.93
 // of the measured copy rate). Softmax in registers, statistics per warp, so the
 // warps never wait for one another inside an item; a row's reference is moved (and
 // the accumulator rescaled) only when a score exceeds it by more than kLazy, so
@@ -469,7 +469,9 @@ cudaError_t launch_attn_decode(const AttnParams& p, const CUtensorMap& k, const 
 cudaError_t attn_decode_error_word(unsigned** word) { return cudaGetSymbolAddress((void**)word, g_attn_err); }
 
 // Promotion to 128 bytes: a head's row is 3 lines at 192 channels, and its neighbours
-// are read much later (with 256 bytes the step above took 465 us).
+// are read much later (with 256 bytes the step above took 465 us). A row that is no
+// multiple of 128 bytes shares lines with its neighbours: of 80 channels, 664 MB are
+// fetched for 444; other promotions were not measured there.
 bool attn_cache_map(CUtensorMap* m, const void* cache, const AttnParams& p) {
   sm100::EncodeTiledFn f = sm100::encode_fn();
   if (!f) return false;
