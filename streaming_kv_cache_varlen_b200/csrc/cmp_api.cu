@@ -274,7 +274,7 @@ __global__ void take_words_kernel(unsigned* kv, unsigned* decode, unsigned* chun
   g_taken = atomicExch(kv, 0u) | atomicExch(decode, 0u) | atomicExch(chunk, 0u);
 }
 
-// The current device's words, read and cleared, by way of stream s.
+// The current device's words, read and cleared, by way of stream s if it is that device's.
 cudaError_t take_device_words(cudaStream_t s, unsigned* word) {
   static std::mutex mu;  // g_taken belongs to one call until it is read
   std::lock_guard<std::mutex> lk(mu);
@@ -282,7 +282,11 @@ cudaError_t take_device_words(cudaStream_t s, unsigned* word) {
   cudaError_t e = cmp::kv_error_word(&kv);
   if (e == cudaSuccess) e = cmp::attn_decode_error_word(&decode);
   if (e == cudaSuccess) e = cmp::attn_chunk_error_word(&chunk);
+  int here = 0, of_s = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&here);
+  if (e == cudaSuccess) e = cudaStreamGetDevice(s, &of_s);
   if (e != cudaSuccess) return e;
+  if (of_s != here) s = cudaStreamPerThread;
   take_words_kernel<<<1, 1, 0, s>>>(kv, decode, chunk);
   e = cudaGetLastError();
   if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(word, g_taken, sizeof(*word), 0, cudaMemcpyDeviceToHost, s);
